@@ -246,9 +246,11 @@ mxattn_status mxattn_forward_noalloc(const void* Q, const void* K, const void* V
 
 /*
  * Synchronizes `stream`, reads the status word of `workspace` (written by
- * the last forward that used it) and returns MXATTN_OK or
- * MXATTN_ERR_TIMEOUT.  MXATTN_ERR_CUDA if the synchronization or copy fails.
- * The word is reset by the next forward on this workspace.
+ * the last forward that used it) and returns MXATTN_OK,
+ * MXATTN_ERR_TIMEOUT, or MXATTN_ERR_INVALID (serving operators: an offset,
+ * length or page index was out of range).  MXATTN_ERR_CUDA if the
+ * synchronization or copy fails.  The word is reset by the next forward on
+ * this workspace; the serving operators only add to it.
  */
 mxattn_status mxattn_workspace_status(const void* workspace, mxattn_stream_t stream);
 
@@ -382,6 +384,119 @@ mxattn_status mxattn_p_selftest(int path, const float* in, int64_t n, float qmax
  */
 mxattn_status mxattn_mxf4_mma_loop(int ctas, int iters, uint32_t* status, uint64_t* cycles,
                                    mxattn_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Serving operators: attention over packed prompts, an 8-bit paged cache of
+ * keys and values, and single-token attention over it (the paper has no
+ * counterpart: it treats one bidirectional sequence length).
+ *
+ * Common to them:
+ *   - 16-bit operands and outputs of one type, `dtype`; d in {64, 128}; Hq a
+ *     multiple of Hkv (query head h reads key head h / (Hq / Hkv)).
+ *   - Tensors [rows, heads, d] with contiguous rows of d elements and, for the
+ *     rest, strides in elements: `strides` (a host array, read during the
+ *     call; NULL: dense tensors) lists a row stride and a head stride for each
+ *     tensor, in the order each call names.  Strides are multiples of 8 and at
+ *     least d; base pointers are 16-byte aligned.
+ *   - Offsets, lengths and block tables are device int32, read by the kernels
+ *     (no host synchronization, so a captured graph replays with new ones).
+ *     One that is out of range never leads to an access outside the tensors:
+ *     it is brought into range or the page left out as described, and
+ *     MXATTN_ERR_INVALID is ORed into the status word.
+ *   - The status word is the first u32 of the workspace.  These calls only
+ *     add to it: its owner zeroes it when the workspace is allocated (or to
+ *     clear an error), and mxattn_workspace_status reads it.
+ *   - A workspace serves one call at a time: calls that may overlap on the GPU
+ *     (streams, or graphs that replay at the same time) take one each.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { MXATTN_BF16 = 0, MXATTN_FP16 = 1 } mxattn_dtype;
+
+/*
+ * Attention over a packed batch of prompts.  Sequence b's queries are rows
+ * q_offsets[b] .. q_offsets[b + 1] - 1 of Q and O, its keys rows kv_offsets[b]
+ * .. kv_offsets[b + 1] - 1 of K and V (n queries, m keys; pass the same offsets
+ * twice where they agree):
+ *   s_ij = softmax_scale * q_i . k_j over the keys j that query i sees -- all m,
+ *          or with causal = 1 those with j <= i + m - n (the queries are the
+ *          newest n tokens, so m > n is a prompt's later chunk),
+ *   O_i  = sum_j e^(s_ij) v_j / sum_j e^(s_ij),   lse_i = ln sum_j e^(s_ij).
+ * A query that sees no key gets O = 0 and lse = -inf.  Keys a query does not
+ * see do not reach it, whatever they hold (NaN and infinities too); rows of O
+ * and lse that belong to no sequence are left as they were.
+ *   Q, O: [total_q, Hq, d]; K, V: [total_kv, Hkv, d]; lse: fp32 [Hq, lse_stride]
+ *   with lse_stride >= total_q, or NULL.
+ *   strides: {Q row, Q head, K row, K head, V row, V head, O row, O head}.
+ *   offsets: device int32 [B + 1], non-decreasing, within [0, total].
+ *   softmax_scale <= 0 selects 1/sqrt(d).  total_q, total_kv <= 2^30.
+ *   workspace: >= mxattn_prompt_workspace_size() bytes, 256-byte aligned.
+ * Scores, maxima and sums are fp32; e^(s - max) is rounded to `dtype` for the
+ * product with V; O is rounded once.  total_q = 0 or B = 0 launches nothing.
+ * Errors: MXATTN_ERR_INVALID (null, misaligned, sizes, strides, small
+ * workspace), MXATTN_ERR_UNSUPPORTED (d, sizes beyond the limits),
+ * MXATTN_ERR_CUDA.
+ */
+size_t mxattn_prompt_workspace_size(void);
+mxattn_status mxattn_prompt(const void* Q, const void* K, const void* V, mxattn_dtype dtype, const int32_t* q_offsets,
+                            const int32_t* kv_offsets, int B, int64_t total_q, int64_t total_kv, int Hq, int Hkv,
+                            int d, const int64_t* strides, int causal, float softmax_scale, void* O, float* lse,
+                            int64_t lse_stride, void* workspace, size_t workspace_bytes, mxattn_stream_t stream);
+
+/*
+ * The 8-bit paged cache.  A pool of num_pages pages of `page` tokens (16, 32,
+ * 64 or 128):
+ *   k_codes, v_codes: u8 [num_pages, Hkv, page, d], OCP FP8 E4M3, 16-byte aligned;
+ *   k_scales, v_scales: u8 [num_pages, Hkv], E8M0: a value is code * 2^(byte - 127).
+ * block_table: device int32, row b (stride table_stride >= max_pages) lists the
+ * pages of sequence b: its token at position t is slot t % page of page
+ * block_table[b][t / page].
+ *
+ * mxattn_cache_store writes new tokens behind the ones a sequence has:
+ * sequence b's rows offsets[b] .. offsets[b + 1] - 1 of K and V go to positions
+ * held_lens[b], held_lens[b] + 1, ...  (one row each for a decode step, whole
+ * prompts, or both mixed).  For each page and head that gets tokens:
+ *   e = the smallest integer in [-127, 127] with amax <= 448 * 2^e over the new
+ *       tokens, and no less than the page's exponent if it holds earlier tokens
+ *       of the sequence (slots below the new ones); where that raises the
+ *       exponent, those tokens' codes c become E4M3(c * 2^(old e - e));
+ *   code = E4M3(x * 2^-e), to nearest, ties to even, saturating; NaN stays NaN.
+ * Slots behind the new tokens are left as they were.  held_lens is not updated.
+ *   K, V: [tokens, Hkv, d]; strides: {K row, K head, V row, V head}.
+ *   status: device u32 that MXATTN_ERR_INVALID is ORed into (or NULL).  A
+ *   sequence whose length is negative or would pass max_pages * page, and
+ *   a page index outside the pool, store nothing.
+ * Pages that get tokens belong to one sequence of the batch each: storing to
+ * one page from two sequences in a call is a race.  max_pages * page <= 2^30.
+ * tokens = 0 or B = 0 launches nothing.  Errors as mxattn_prompt.
+ */
+mxattn_status mxattn_cache_store(const void* K, const void* V, mxattn_dtype dtype, int64_t tokens,
+                                 const int32_t* offsets, const int32_t* held_lens, int B, int Hkv, int d,
+                                 const int64_t* strides, uint8_t* k_codes, uint8_t* v_codes, uint8_t* k_scales,
+                                 uint8_t* v_scales, int num_pages, int page, const int32_t* block_table,
+                                 int64_t table_stride, int max_pages, uint32_t* status, mxattn_stream_t stream);
+
+/*
+ * Single-token attention over the cache: the query of sequence b (row b of Q)
+ * sees its first lens[b] cached tokens (store the step's token first):
+ *   O_b = softmax(softmax_scale * q_b K^T) V,  lse_b as for mxattn_prompt.
+ * lens[b] = 0 gives O = 0 and lse = -inf.  Slots and pages behind a sequence's
+ * length are never read into a result, whatever they hold; block_table entries
+ * behind its last page are not read.  Pages may be shared by sequences.
+ *   Q, O: [B, Hq, d]; lse: fp32 [B, Hq] or NULL; strides: {Q row, Q head, O row,
+ *   O head}; lens: device int32 [B]; softmax_scale <= 0 selects 1/sqrt(d).
+ *   workspace: >= mxattn_cache_attend_workspace_size(Hq, Hkv, d) bytes (it does
+ *   not depend on B or the lengths), 256-byte aligned.
+ * A length that is negative counts as 0, one beyond max_pages * page as that;
+ * tokens of a page outside the pool are left out; each is reported in the
+ * status word.  Errors as mxattn_prompt.
+ */
+size_t mxattn_cache_attend_workspace_size(int Hq, int Hkv, int d);
+mxattn_status mxattn_cache_attend(const void* Q, mxattn_dtype dtype, int B, int Hq, int Hkv, int d,
+                                  const int64_t* strides, const uint8_t* k_codes, const uint8_t* v_codes,
+                                  const uint8_t* k_scales, const uint8_t* v_scales, int num_pages, int page,
+                                  const int32_t* block_table, int64_t table_stride, int max_pages,
+                                  const int32_t* lens, float softmax_scale, void* O, float* lse, void* workspace,
+                                  size_t workspace_bytes, mxattn_stream_t stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char* mxattn_status_string(mxattn_status status);

@@ -13,6 +13,8 @@ from .mxattn import (  # noqa: F401
     forward_host_workspace_size,
     host_groups,
     mxattn_attend,
+    mxattn_cache_attend,
+    mxattn_cache_store,
     mxattn_forward,
     mxattn_forward_noalloc,
     mxattn_forward_quantized,
@@ -23,13 +25,17 @@ from .mxattn import (  # noqa: F401
     mxattn_mxf4_mma_loop,
     mxattn_p_selftest,
     mxattn_prepare,
+    mxattn_prompt,
     mxattn_quantize,
     mxattn_quantize_vt,
     mxattn_status_string,
     mxattn_wait_selftest,
     mxattn_workspace_size,
     mxattn_workspace_status,
+    new_cache,
+    new_cache_attend_workspace,
     new_nvfp4_workspace,
+    new_prompt_workspace,
     new_workspace,
     nvfp4_workspace_layout,
     nvfp4_workspace_size,

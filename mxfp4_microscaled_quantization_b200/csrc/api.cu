@@ -282,7 +282,7 @@ MXATTN_API mxattn_status mxattn_workspace_status(const void* workspace, mxattn_s
     if (cudaStreamSynchronize(s) != cudaSuccess) return MXATTN_ERR_CUDA;
     uint32_t word = 0;
     if (cudaMemcpy(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return MXATTN_ERR_CUDA;
-    return (word & 4u) ? MXATTN_ERR_TIMEOUT : MXATTN_OK;
+    return (word & 4u) ? MXATTN_ERR_TIMEOUT : (word & 1u) ? MXATTN_ERR_INVALID : MXATTN_OK;
 }
 
 // ------------------------------------------------------------------ NVFP4 comparison variant

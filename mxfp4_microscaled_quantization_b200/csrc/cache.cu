@@ -1,0 +1,206 @@
+// cache.cu -- the 8-bit paged cache of keys and values: storing tokens.
+//
+// A page holds `page` tokens of every key head; for each page and head, K and
+// V apart, the cache keeps E4M3 codes and one power of two 2^e, the value being
+// code * 2^e.  e is the smallest integer in [-127, 127] with amax <= 448 * 2^e
+// (448: the largest E4M3 value) over the tokens in that page and head: the
+// rule of the library's MXFP4 blocks with E4M3's boundary.  A power of two
+// costs an element format with an exponent of its own no precision, and lets a
+// page's exponent grow under codes that are already there: code' = code *
+// 2^(e - e'), which only rounds where a code reaches E4M3's subnormals.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.cuh"
+#include "serve.cuh"
+
+namespace mxattn {
+namespace {
+
+// Smallest e with amax <= 448 * 2^e for amax >= 0 in fp32 (448 = 1.75 * 2^8):
+// floor(log2 amax) - 8, plus one where the significand exceeds 1.75.  amax = 0
+// gives -127; fp16's subnormals are normal numbers in fp32, and bf16's end at
+// the clamp.
+__device__ __forceinline__ int page_exponent(float amax) {
+    const uint32_t bits = __float_as_uint(amax);
+    const int E = static_cast<int>(bits >> 23);
+    if (E == 0) return -127;
+    const int e = E - 135 + (((bits & 0x7FFFFFu) > 0x600000u) ? 1 : 0);
+    return min(max(e, -127), 127);
+}
+
+// Two fp32 values to two E4M3 codes (lo in the low byte): nearest even, beyond
+// +-448 saturated, NaN stays NaN.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ void unpack_e4m3x2(uint32_t b, float& lo, float& hi) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(b)));
+    widen2<true>(h2, lo, hi);
+}
+
+constexpr int kStoreThreads = 256;
+
+// A block per (page that gets tokens, key head, K or V).  blockIdx.x counts the
+// pages that the batch's sequences touch; the block finds its sequence with a
+// scan over the batch.
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kStoreThreads) cache_store_kernel(const __grid_constant__ StoreArgs a) {
+    constexpr int CH = D / 8;  // 16-byte chunks of a token's row
+    __shared__ int s_scan[kStoreThreads / 32];
+    __shared__ int s_item[4];  // sequence, its pages before this one, first and last source row
+    __shared__ float s_amax[kStoreThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int page = a.page, P = a.page_shift;
+
+    if (tid == 0) s_item[0] = -1;
+    __syncthreads();
+    int before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kStoreThreads) {
+        const int b = b0 + tid;
+        int begin = 0, end = 0, held = 0, count = 0;
+        if (b < a.B) {
+            bool ok = packed_range(a.offsets, b, a.tokens, begin, end);
+            held = a.held[b];
+            // a length that is negative or runs past the sequence's block table stores nothing
+            if (held < 0 || static_cast<int64_t>(held) + (end - begin) > static_cast<int64_t>(a.max_pages) << P) {
+                ok = false;
+                end = begin;
+            }
+            if (!ok && a.status != nullptr && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, kStatusInvalid);
+            if (end > begin) count = ((held + end - begin - 1) >> P) - (held >> P) + 1;
+        }
+        int incl = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int w = 0; w < kStoreThreads / 32; ++w) {
+            if (w < warp) incl += s_scan[w];
+            total += s_scan[w];
+        }
+        const int item = static_cast<int>(blockIdx.x) - before;
+        if (item >= incl - count && item < incl) {
+            const int nth = item - (incl - count);  // this page among the sequence's touched pages
+            s_item[0] = b;
+            s_item[1] = (held >> P) + nth;
+            const int lo = max(held, s_item[1] << P);  // positions [lo, hi) of this page get tokens
+            const int hi = min(held + end - begin, (s_item[1] + 1) << P);
+            s_item[2] = begin + lo - held;
+            s_item[3] = (lo & (page - 1)) | (hi - lo) << 16;
+        }
+        before += total;
+        __syncthreads();
+        if (s_item[0] >= 0 || static_cast<int>(blockIdx.x) < before) break;
+    }
+    if (s_item[0] < 0) return;
+    const int pg = a.table[static_cast<int64_t>(s_item[0]) * a.table_stride + s_item[1]];
+    if (pg < 0 || pg >= a.num_pages) {
+        if (tid == 0 && a.status != nullptr) atomicOr(a.status, kStatusInvalid);
+        return;
+    }
+    const int src = s_item[2], slot = s_item[3] & 0xFFFF, n = s_item[3] >> 16;
+    const int h = blockIdx.y >> 1;
+    const bool is_v = blockIdx.y & 1;
+    const uint16_t* x = is_v ? a.v + src * a.v_token + h * a.v_head : a.k + src * a.k_token + h * a.k_head;
+    const int64_t stride = is_v ? a.v_token : a.k_token;
+    const int64_t cell = static_cast<int64_t>(pg) * a.Hkv + h;
+    uint8_t* codes = (is_v ? a.v_codes : a.k_codes) + cell * page * D;
+    uint8_t* scale = (is_v ? a.v_scales : a.k_scales) + cell;
+
+    // At most 128 * D / 8 chunks a page: 8 of a thread.
+    constexpr int kMost = 128 * CH / kStoreThreads;
+    uint4 raw[kMost];
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int c = tid + i * kStoreThreads;
+        if (c < n * CH) raw[i] = *reinterpret_cast<const uint4*>(x + (c / CH) * stride + (c % CH) * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        if (tid + i * kStoreThreads < n * CH) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float lo, hi;
+                widen2<FP16>(w[j], lo, hi);
+                amax = fmaxf(amax, fmaxf(fabsf(lo), fabsf(hi)));
+            }
+        }
+    }
+    amax = warp_max(amax);
+    if (lane == 0) s_amax[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kStoreThreads / 32; ++w) amax = fmaxf(amax, s_amax[w]);
+    int e = page_exponent(amax);
+    if (slot > 0) {
+        // Tokens below: the exponent never falls, and where it rises their codes are rounded to the new one.
+        const int old = static_cast<int>(*scale) - 127;
+        e = max(e, old);
+        if (e > old) {
+            const float down = exp2f(static_cast<float>(max(old - e, -126)));  // 2^-126 turns every code to 0 as well
+            for (int c = tid; c < slot * CH; c += kStoreThreads) {
+                uint2 w = *reinterpret_cast<const uint2*>(codes + c * 8);
+                uint32_t in[2] = {w.x, w.y}, out[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float f[4];
+                    unpack_e4m3x2(in[j] & 0xFFFFu, f[0], f[1]);
+                    unpack_e4m3x2(in[j] >> 16, f[2], f[3]);
+                    out[j] = pack_e4m3x2(f[0] * down, f[1] * down) | pack_e4m3x2(f[2] * down, f[3] * down) << 16;
+                }
+                *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(out[0], out[1]);
+            }
+        }
+    }
+    const float inv = exp2_neg_int(e);
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int c = tid + i * kStoreThreads;
+        if (c < n * CH) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            uint32_t out[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float f[4];
+                widen2<FP16>(w[2 * j], f[0], f[1]);
+                widen2<FP16>(w[2 * j + 1], f[2], f[3]);
+                out[j] = pack_e4m3x2(f[0] * inv, f[1] * inv) | pack_e4m3x2(f[2] * inv, f[3] * inv) << 16;
+            }
+            *reinterpret_cast<uint2*>(codes + (slot * CH + c) * 8) = make_uint2(out[0], out[1]);
+        }
+    }
+    __syncthreads();  // every thread has read the old exponent
+    if (tid == 0) *scale = static_cast<uint8_t>(e + 127);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_store(const StoreArgs& a, cudaStream_t stream) {
+    if (a.tokens == 0 || a.B == 0) return cudaSuccess;
+    // Pages that B sequences with `tokens` tokens in all can touch.
+    const int64_t items = min(a.tokens, (a.tokens >> a.page_shift) + 2 * static_cast<int64_t>(a.B));
+    const dim3 grid(static_cast<unsigned>(items), 2 * a.Hkv);
+    if (a.d == 128) {
+        if (a.fp16) cache_store_kernel<128, true><<<grid, kStoreThreads, 0, stream>>>(a);
+        else cache_store_kernel<128, false><<<grid, kStoreThreads, 0, stream>>>(a);
+    } else {
+        if (a.fp16) cache_store_kernel<64, true><<<grid, kStoreThreads, 0, stream>>>(a);
+        else cache_store_kernel<64, false><<<grid, kStoreThreads, 0, stream>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace mxattn

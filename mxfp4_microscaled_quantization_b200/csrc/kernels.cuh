@@ -87,4 +87,63 @@ cudaError_t launch_nv_quantize_rows(const void* x, int64_t rows, int64_t cols, u
 // The fused attention kernel.  Returns cudaSuccess or the launch / encode error.
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
 
+// Attention over packed prompts (16-bit operands).  Pointers and strides in
+// elements of 16 bits; offsets int32 [B + 1].
+struct PromptArgs {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* o;
+    float* lse;  // [Hq, lse_head], may be null
+    const int32_t* q_offsets;
+    const int32_t* kv_offsets;
+    uint32_t* status;
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head, lse_head;
+    int64_t total_q, total_kv;
+    int B, Hq, Hkv, d;
+    int causal;
+    int fp16;
+    float scale;
+};
+cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t stream);
+
+// Storing tokens in the 8-bit paged cache.
+struct StoreArgs {
+    const uint16_t* k;
+    const uint16_t* v;
+    const int32_t* offsets;  // [B + 1] rows of k and v
+    const int32_t* held;     // [B] tokens that each sequence has in the cache before
+    const int32_t* table;    // [B, table_stride] page indexes
+    uint8_t* k_codes;        // [num_pages, Hkv, page, d]
+    uint8_t* v_codes;
+    uint8_t* k_scales;       // [num_pages, Hkv]
+    uint8_t* v_scales;
+    uint32_t* status;        // may be null
+    int64_t k_token, k_head, v_token, v_head, table_stride, tokens;
+    int B, Hkv, d, page, page_shift, max_pages, num_pages;
+    int fp16;
+};
+cudaError_t launch_cache_store(const StoreArgs& a, cudaStream_t stream);
+
+// Single-token attention over the cache.
+struct AttendArgs {
+    const uint16_t* q;  // one row a sequence
+    uint16_t* o;
+    float* lse;         // [B, Hq], may be null
+    const uint8_t* k_codes;
+    const uint8_t* v_codes;
+    const uint8_t* k_scales;
+    const uint8_t* v_scales;
+    const int32_t* table;
+    const int32_t* lens;
+    uint32_t* status;
+    void* scratch;      // behind the status word
+    int64_t q_seq, q_head, o_seq, o_head, table_stride;
+    int B, Hq, Hkv, d, page, page_shift, max_pages, num_pages;
+    int fp16;
+    float scale;
+};
+size_t cache_attend_scratch_bytes(int Hq, int Hkv, int d);
+cudaError_t launch_cache_attend(const AttendArgs& a, cudaStream_t stream);
+
 }  // namespace mxattn

@@ -1,0 +1,173 @@
+// serve_api.cu -- the C ABI of the serving operators (declared in
+// include/mxattn.h): argument checks, then the launchers.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "kernels.cuh"
+#include "mxattn.h"
+
+#define MXATTN_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+constexpr size_t kStatusBytes = 256;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // rows of a packed batch: row indexes stay in 32 bits
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Strides in elements of a [tokens, heads, d] tensor whose rows of d elements
+// are contiguous: 16-byte rows, and no two rows on top of each other.
+bool strides_ok(int64_t token, int64_t head, int d) {
+    return token >= d && head >= d && token % 8 == 0 && head % 8 == 0 && token < (int64_t(1) << 40) &&
+           head < (int64_t(1) << 40);
+}
+
+mxattn_status check_heads(int B, int Hq, int Hkv, int d, mxattn_dtype dtype) {
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return MXATTN_ERR_INVALID;
+    if (dtype != MXATTN_BF16 && dtype != MXATTN_FP16) return MXATTN_ERR_INVALID;
+    if (d != 64 && d != 128) return MXATTN_ERR_UNSUPPORTED;
+    if (Hq > 65535 || Hkv > 32767 || B > (1 << 20)) return MXATTN_ERR_UNSUPPORTED;
+    return MXATTN_OK;
+}
+
+float resolve_scale(float s, int d) { return (s > 0.f) ? s : static_cast<float>(1.0 / std::sqrt(static_cast<double>(d))); }
+
+int page_shift(int page) {
+    for (int p = 4; p <= 7; ++p)
+        if (page == 1 << p) return p;
+    return -1;
+}
+
+}  // namespace
+
+MXATTN_API size_t mxattn_prompt_workspace_size(void) { return kStatusBytes; }
+
+MXATTN_API mxattn_status mxattn_prompt(const void* Q, const void* K, const void* V, mxattn_dtype dtype,
+                                       const int32_t* q_offsets, const int32_t* kv_offsets, int B, int64_t total_q,
+                                       int64_t total_kv, int Hq, int Hkv, int d, const int64_t* strides, int causal,
+                                       float softmax_scale, void* O, float* lse, int64_t lse_stride, void* workspace,
+                                       size_t workspace_bytes, mxattn_stream_t stream) {
+    const mxattn_status st = check_heads(B, Hq, Hkv, d, dtype);
+    if (st != MXATTN_OK) return st;
+    if (total_q < 0 || total_kv < 0 || (causal != 0 && causal != 1)) return MXATTN_ERR_INVALID;
+    if (total_q > kMaxTokens || total_kv > kMaxTokens) return MXATTN_ERR_UNSUPPORTED;
+    if (workspace == nullptr || workspace_bytes < kStatusBytes || !aligned(workspace, 256)) return MXATTN_ERR_INVALID;
+    if (B == 0 || total_q == 0) return MXATTN_OK;
+    if (Q == nullptr || O == nullptr || q_offsets == nullptr || kv_offsets == nullptr) return MXATTN_ERR_INVALID;
+    if (total_kv > 0 && (K == nullptr || V == nullptr)) return MXATTN_ERR_INVALID;
+    if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16) || !aligned(lse, 4) ||
+        !aligned(q_offsets, 4) || !aligned(kv_offsets, 4))
+        return MXATTN_ERR_INVALID;
+    if (lse != nullptr && lse_stride < total_q) return MXATTN_ERR_INVALID;
+    const int64_t dense[8] = {int64_t(Hq) * d, d, int64_t(Hkv) * d, d, int64_t(Hkv) * d, d, int64_t(Hq) * d, d};
+    const int64_t* s = strides != nullptr ? strides : dense;
+    for (int i = 0; i < 8; i += 2)
+        if (!strides_ok(s[i], s[i + 1], d)) return MXATTN_ERR_INVALID;
+    mxattn::PromptArgs a{};
+    a.q = static_cast<const uint16_t*>(Q);
+    a.k = static_cast<const uint16_t*>(K);
+    a.v = static_cast<const uint16_t*>(V);
+    a.o = static_cast<uint16_t*>(O);
+    a.lse = lse;
+    a.q_offsets = q_offsets;
+    a.kv_offsets = kv_offsets;
+    a.status = static_cast<uint32_t*>(workspace);
+    a.q_token = s[0], a.q_head = s[1], a.k_token = s[2], a.k_head = s[3];
+    a.v_token = s[4], a.v_head = s[5], a.o_token = s[6], a.o_head = s[7];
+    a.lse_head = lse_stride;
+    a.total_q = total_q;
+    a.total_kv = total_kv;
+    a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.d = d;
+    a.causal = causal;
+    a.fp16 = dtype == MXATTN_FP16;
+    a.scale = resolve_scale(softmax_scale, d);
+    return mxattn::launch_prompt(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MXATTN_OK : MXATTN_ERR_CUDA;
+}
+
+MXATTN_API mxattn_status mxattn_cache_store(const void* K, const void* V, mxattn_dtype dtype, int64_t tokens,
+                                            const int32_t* offsets, const int32_t* held_lens, int B, int Hkv, int d,
+                                            const int64_t* strides, uint8_t* k_codes, uint8_t* v_codes,
+                                            uint8_t* k_scales, uint8_t* v_scales, int num_pages, int page,
+                                            const int32_t* block_table, int64_t table_stride, int max_pages,
+                                            uint32_t* status, mxattn_stream_t stream) {
+    const mxattn_status st = check_heads(B, Hkv, Hkv, d, dtype);
+    if (st != MXATTN_OK) return st;
+    if (tokens < 0 || num_pages < 0 || max_pages < 0 || table_stride < max_pages) return MXATTN_ERR_INVALID;
+    const int shift = page_shift(page);
+    if (shift < 0 || tokens > kMaxTokens || int64_t(max_pages) * page > kMaxTokens) return MXATTN_ERR_UNSUPPORTED;
+    if (B == 0 || tokens == 0) return MXATTN_OK;
+    if (!K || !V || !offsets || !held_lens || !k_codes || !v_codes || !k_scales || !v_scales || !block_table)
+        return MXATTN_ERR_INVALID;
+    if (!aligned(K, 16) || !aligned(V, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(offsets, 4) ||
+        !aligned(held_lens, 4) || !aligned(block_table, 4) || !aligned(status, 4))
+        return MXATTN_ERR_INVALID;
+    const int64_t dense[4] = {int64_t(Hkv) * d, d, int64_t(Hkv) * d, d};
+    const int64_t* s = strides != nullptr ? strides : dense;
+    if (!strides_ok(s[0], s[1], d) || !strides_ok(s[2], s[3], d)) return MXATTN_ERR_INVALID;
+    mxattn::StoreArgs a{};
+    a.k = static_cast<const uint16_t*>(K);
+    a.v = static_cast<const uint16_t*>(V);
+    a.offsets = offsets;
+    a.held = held_lens;
+    a.table = block_table;
+    a.k_codes = k_codes, a.v_codes = v_codes, a.k_scales = k_scales, a.v_scales = v_scales;
+    a.status = status;
+    a.k_token = s[0], a.k_head = s[1], a.v_token = s[2], a.v_head = s[3];
+    a.table_stride = table_stride;
+    a.tokens = tokens;
+    a.B = B, a.Hkv = Hkv, a.d = d, a.page = page, a.page_shift = shift;
+    a.max_pages = max_pages, a.num_pages = num_pages;
+    a.fp16 = dtype == MXATTN_FP16;
+    return mxattn::launch_cache_store(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MXATTN_OK
+                                                                                               : MXATTN_ERR_CUDA;
+}
+
+MXATTN_API size_t mxattn_cache_attend_workspace_size(int Hq, int Hkv, int d) {
+    if (check_heads(1, Hq, Hkv, d, MXATTN_BF16) != MXATTN_OK) return 0;
+    return kStatusBytes + mxattn::cache_attend_scratch_bytes(Hq, Hkv, d);
+}
+
+MXATTN_API mxattn_status mxattn_cache_attend(const void* Q, mxattn_dtype dtype, int B, int Hq, int Hkv, int d,
+                                             const int64_t* strides, const uint8_t* k_codes, const uint8_t* v_codes,
+                                             const uint8_t* k_scales, const uint8_t* v_scales, int num_pages, int page,
+                                             const int32_t* block_table, int64_t table_stride, int max_pages,
+                                             const int32_t* lens, float softmax_scale, void* O, float* lse,
+                                             void* workspace, size_t workspace_bytes, mxattn_stream_t stream) {
+    const mxattn_status st = check_heads(B, Hq, Hkv, d, dtype);
+    if (st != MXATTN_OK) return st;
+    if (num_pages < 0 || max_pages < 0 || table_stride < max_pages) return MXATTN_ERR_INVALID;
+    const int shift = page_shift(page);
+    if (shift < 0 || int64_t(max_pages) * page > kMaxTokens) return MXATTN_ERR_UNSUPPORTED;
+    if (workspace == nullptr || !aligned(workspace, 256) ||
+        workspace_bytes < kStatusBytes + mxattn::cache_attend_scratch_bytes(Hq, Hkv, d))
+        return MXATTN_ERR_INVALID;
+    if (B == 0) return MXATTN_OK;
+    if (!Q || !O || !lens) return MXATTN_ERR_INVALID;
+    if (max_pages > 0 && !block_table) return MXATTN_ERR_INVALID;
+    if (num_pages > 0 && (!k_codes || !v_codes || !k_scales || !v_scales)) return MXATTN_ERR_INVALID;
+    if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(lens, 4) ||
+        !aligned(block_table, 4) || !aligned(lse, 4))
+        return MXATTN_ERR_INVALID;
+    const int64_t dense[4] = {int64_t(Hq) * d, d, int64_t(Hq) * d, d};
+    const int64_t* s = strides != nullptr ? strides : dense;
+    if (!strides_ok(s[0], s[1], d) || !strides_ok(s[2], s[3], d)) return MXATTN_ERR_INVALID;
+    mxattn::AttendArgs a{};
+    a.q = static_cast<const uint16_t*>(Q);
+    a.o = static_cast<uint16_t*>(O);
+    a.lse = lse;
+    a.k_codes = k_codes, a.v_codes = v_codes, a.k_scales = k_scales, a.v_scales = v_scales;
+    a.table = block_table;
+    a.lens = lens;
+    a.status = static_cast<uint32_t*>(workspace);
+    a.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
+    a.q_seq = s[0], a.q_head = s[1], a.o_seq = s[2], a.o_head = s[3];
+    a.table_stride = table_stride;
+    a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.d = d, a.page = page, a.page_shift = shift;
+    a.max_pages = max_pages, a.num_pages = num_pages;
+    a.fp16 = dtype == MXATTN_FP16;
+    a.scale = resolve_scale(softmax_scale, d);
+    return mxattn::launch_cache_attend(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MXATTN_OK
+                                                                                                : MXATTN_ERR_CUDA;
+}
