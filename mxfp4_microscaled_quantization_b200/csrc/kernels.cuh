@@ -87,6 +87,10 @@ cudaError_t launch_nv_quantize_rows(const void* x, int64_t rows, int64_t cols, u
 // The fused attention kernel.  Returns cudaSuccess or the launch / encode error.
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
 
+// Devices whose per-device set-up a launcher remembers, and a device's SMs.
+constexpr int kMaxDevices = 64;
+int sm_count(int dev);
+
 // Attention over packed prompts (16-bit operands).  Pointers and strides in
 // elements of 16 bits; offsets int32 [B + 1].
 struct PromptArgs {

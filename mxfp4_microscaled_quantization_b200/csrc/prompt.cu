@@ -1,12 +1,51 @@
-// prompt.cu -- attention over packed prompts of different lengths (16-bit
-// operands, grouped heads, causal or not).
+// prompt.cu -- attention over packed prompts of different lengths for sm_100a
+// (16-bit operands, grouped heads, causal or not).
 //
 // For sequence b with n queries and m keys, query i and head h (key head g = h
 // / (Hq / Hkv)):  s_ij = scale q_i . k_j over the keys j it sees (causal: j <=
 // i + m - n, the queries being the newest n tokens),  o_i = sum_j e^(s_ij - M)
 // v_j / sum_j e^(s_ij - M),  lse_i = M + ln sum_j e^(s_ij - M).  A row that
 // sees no key gives zeros and -inf.
+//
+// The work is a list of items, each two 128-row query tiles (A and B) of one
+// key head of one sequence: the tiles (128 tokens of one query head) of the
+// group's Hq / Hkv heads are numbered token block first, head second, from the
+// last block down (the most keys first), and an item takes two in a row, so the
+// two read the same K and V tiles whatever the group's size.  The grid is
+// persistent; block c takes the items c, c + grid, ....  Roles (384 threads):
+//   warps 0-3 / 4-7  softmax of tile A / B, a thread per query row (= TMEM
+//                    lane): the row of S from TMEM, running maximum, P back
+//                    into S's own columns in 16 bits, O rescaled in TMEM only
+//                    when the maximum has grown by more than 2^8, O / l.
+//   warp 8           TMA producer: K and V tiles of 128 keys through one ring
+//                    (K0, V0, K1, ...), Q once an item.
+//   warp 9           MMA issuer: S_t(j) = Q_t K(j)^T and O_t += P_t(j) V(j) in the
+//                    order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1): while one tile's
+//                    softmax runs, the tensor core has the other's two products.
+//                    One thread issues all of them, so the tensor core runs them
+//                    in this order, and S_t(j+1) may overwrite the columns that
+//                    PV_t(j) reads P from.
+//   warp 10          scheduler: finds each item's sequence from the offsets (a
+//                    scan that only moves forward) and publishes the item.
+//
+// Masked places.  Scores of keys that a row does not see are replaced, so K may
+// hold anything there.  V rows behind the sequence's last key are zeroed in
+// shared memory before they are multiplied by P = 0.  Later keys of the row's
+// own sequence in its last tile stay (other rows of the tile see them): should
+// one hold an infinity or NaN, 0 * inf spoils the row's sum, which the epilogue
+// sees (the row sum l, of masked weights, is finite and O is not) and then
+// evaluates the row again, key by key (attend_row).
+//
+// Rounding.  P is rounded to the operands' type, as the product's A operand and V
+// have to be of one type; l sums the unrounded fp32 values.  With the maximum
+// left behind by at most 2^8, P stays below 2^8 and fp16 P cannot overflow.
+//
+// Every mbarrier wait is bounded as in attention.cu: a wait that gives up ORs
+// MXATTN_ERR_TIMEOUT into the status word and raises a flag on which every role
+// leaves, after its own copies and products have landed.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstdint>
 
@@ -16,41 +55,604 @@
 namespace mxattn {
 namespace {
 
-// A warp per (query row, head).
+constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
+
+// One item, as the scheduler publishes it.
+struct Item {
+    int q_row[2];   // first row of Q and O of tile A, B
+    int q_head[2];
+    int rows[2];    // rows of the tile that belong to the sequence (0: no tile B)
+    int n[2];       // key tiles the tile needs
+    int lim0[2];    // keys that the tile's first row sees (may be <= 0)
+    int kv_row, kv_head;
+    int m;          // keys of the sequence
+    int last;       // 1: no more items
+    int pad[2];
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int kChunks = D / 64;                  // 128-byte column chunks of a 16-bit row
+    static constexpr int kTileBytes = 128 * D * 2;          // a Q, K or V tile
+    static constexpr int kChunkBytes = 128 * 128;
+    static constexpr int kSlots = 160 * 1024 / kTileBytes;  // ring of K and V tiles
+    static constexpr int kItems = 2;
+    static constexpr int kThreads = 384;
+    // 384 x 168 registers at launch; softmax warpgroups 224, the other 56 (2 x 128 x 224 + 128 x 56 == 384 x 168).
+    static constexpr uint32_t kLaunchRegs = 168, kSoftRegs = 224, kRoleRegs = 56;
+    static_assert(2 * 128 * kSoftRegs + 128 * kRoleRegs == kThreads * kLaunchRegs, "register split");
+    static constexpr int kOffQ = 0;  // [2]
+    static constexpr int kOffRing = kOffQ + 2 * kTileBytes;
+    static constexpr int kOffItems = kOffRing + kSlots * kTileBytes;
+    static constexpr int kOffBar = kOffItems + kItems * sizeof(Item);
+    // q_full, q_empty, kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2], o_done[2], item_full[kItems],
+    // item_empty[kItems], drain
+    static constexpr int kNumBars = 2 + 2 * kSlots + 6 + 2 * kItems + 1;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+    static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+    // TMEM columns: S (and P) of A and B, O of A and B
+    static constexpr uint32_t kColS = 0, kColO = 256;  // + 128 t, + D t
+};
+
+struct KParams {
+    PromptArgs a;
+    float kq;  // softmax scale * log2(e)
+};
+
+// Of the 16 exponential pairs of 32 columns, this many are computed on the FMA
+// pipe instead of the MUFU.
+constexpr int kFmaPairs = 6;
+__host__ __device__ constexpr bool fma_pair(int q) { return (q * kFmaPairs) % 16 < kFmaPairs; }
+
+// 2^w for two values w <= 8 on the FMA pipe: exp2_fma_x2's range reduction and polynomial (max relative
+// error 2.3e-7) with the clamp at -127, where the exponent field becomes 0: what is below 2^-126 ends as a subnormal
+// below it, which the rounding of P to 16 bits and the row sum take for (nearly) nothing.
+__device__ __forceinline__ void exp2_pair(float w0, float w1, float& v0, float& v1) {
+    w0 = fmaxf(w0, -127.f);
+    w1 = fmaxf(w1, -127.f);
+    uint32_t p0, p1, t0, t1;
+    asm("{\n\t.reg .b64 w, t, n, f, p, c;\n\t"
+        "mov.b64 w, {%4, %5};\n\t"
+        "mov.b64 c, {%6, %6};\n\t"
+        "add.rn.f32x2 t, w, c;\n\t"
+        "sub.rn.f32x2 n, t, c;\n\t"
+        "sub.rn.f32x2 f, w, n;\n\t"
+        "mov.b64 p, {%12, %12};\n\t"
+        "mov.b64 c, {%11, %11};\n\t"
+        "fma.rn.f32x2 p, p, f, c;\n\t"
+        "mov.b64 c, {%10, %10};\n\t"
+        "fma.rn.f32x2 p, p, f, c;\n\t"
+        "mov.b64 c, {%9, %9};\n\t"
+        "fma.rn.f32x2 p, p, f, c;\n\t"
+        "mov.b64 c, {%8, %8};\n\t"
+        "fma.rn.f32x2 p, p, f, c;\n\t"
+        "mov.b64 c, {%7, %7};\n\t"
+        "fma.rn.f32x2 p, p, f, c;\n\t"
+        "mov.b64 {%0, %1}, p;\n\t"
+        "mov.b64 {%2, %3}, t;\n\t}"
+        : "=r"(p0), "=r"(p1), "=r"(t0), "=r"(t1)
+        : "f"(w0), "f"(w1), "f"(12582912.0f),  // 1.5 * 2^23
+          "f"(0x1.000002p+0f), "f"(0x1.62e428p-1f), "f"(0x1.ebf91ap-3f), "f"(0x1.c6b782p-5f), "f"(0x1.3d0ba4p-7f),
+          "f"(0x1.5bc922p-10f));
+    v0 = __uint_as_float(p0 + (t0 << 23));
+    v1 = __uint_as_float(p1 + (t1 << 23));
+}
+
+__device__ __forceinline__ void fadd2(float& o0, float& o1, float a0, float a1) {
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(o0), "=f"(o1)
+        : "f"(o0), "f"(o1), "f"(a0), "f"(a1));
+}
+
 template <int D, bool FP16>
-__global__ void __launch_bounds__(128) prompt_rows_kernel(const __grid_constant__ PromptArgs a) {
-    const int row = blockIdx.x, h = blockIdx.y * 4 + (threadIdx.x >> 5);
-    if (h >= a.Hq) return;
-    for (int b = 0; b < a.B; ++b) {
-        int q0, q1, k0, k1;
-        bool ok = packed_range(a.q_offsets, b, a.total_q, q0, q1);
-        ok &= packed_range(a.kv_offsets, b, a.total_kv, k0, k1);
-        if (!ok && threadIdx.x == 0) atomicOr(a.status, kStatusInvalid);
-        if (row < q0 || row >= q1) continue;
-        const int m = k1 - k0;
-        const int n = a.causal ? max(0, min(m, row - q0 + 1 + m - (q1 - q0))) : m;
-        const int g = h / (a.Hq / a.Hkv);
-        attend_row<D, FP16>(a.q + row * a.q_token + h * a.q_head, a.k + k0 * a.k_token + g * a.k_head,
-                            a.v + k0 * a.v_token + g * a.v_head, a.k_token, a.v_token, n, a.scale,
-                            a.o + row * a.o_token + h * a.o_head,
-                            a.lse == nullptr ? nullptr : a.lse + h * a.lse_head + row);
-        return;
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ KParams p) {
+    using C = Cfg<D>;
+    constexpr int S = C::kSlots;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* sQ = smem + C::kOffQ;
+    uint8_t* sRing = smem + C::kOffRing;
+    Item* items = reinterpret_cast<Item*>(smem + C::kOffItems);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint64_t* bar_q_full = bars;
+    uint64_t* bar_q_empty = bars + 1;
+    uint64_t* bar_kv_full = bars + 2;
+    uint64_t* bar_kv_empty = bar_kv_full + S;
+    uint64_t* bar_s_full = bar_kv_empty + S;
+    uint64_t* bar_p_full = bar_s_full + 2;
+    uint64_t* bar_o_done = bar_p_full + 2;
+    uint64_t* bar_item_full = bar_o_done + 2;
+    uint64_t* bar_item_empty = bar_item_full + C::kItems;
+    uint64_t* bar_drain = bar_item_empty + C::kItems;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+    uint32_t* status = p.a.status;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        mbar_init(bar_q_full, 1);
+        mbar_init(bar_q_empty, 1);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(bar_kv_full + s, 1);
+            mbar_init(bar_kv_empty + s, 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bar_s_full + t, 1);
+            mbar_init(bar_p_full + t, 128);
+            mbar_init(bar_o_done + t, 1);
+        }
+        for (int s = 0; s < C::kItems; ++s) {
+            mbar_init(bar_item_full + s, 1);
+            mbar_init(bar_item_empty + s, 10);  // producer, MMA issuer, 8 softmax warps
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
     }
+    if (warp == 9) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tbase = *tmem_holder;
+
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu,
+                          mbar_wait_bounded(bar, parity, abort_flag, status, kStatusTimeout, kTimeoutNs));
+    };
+    // The item that the role takes next (k-th); false: no more, or given up.
+    auto next_item = [&](int k, Item& it) -> bool {
+        const int s = k % C::kItems;
+        if (!wait(bar_item_full + s, (k / C::kItems) & 1)) return false;
+        it = items[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_item_empty + s);
+        return it.last == 0;
+    };
+
+    if (warp >= 8) {
+        warpgroup_regs_dec<C::kRoleRegs>();
+        const bool leader = elect_one_sync();
+        if (warp == 8) {
+            // ------------------------------------------------------------ TMA producer
+            int slot = 0;          // running number of K and V tiles
+            Item it;
+            auto load_kv = [&](const CUtensorMap* map, int j) -> bool {
+                const int s = slot % S;
+                if (slot >= S && !wait(bar_kv_empty + s, ((slot / S) - 1) & 1)) return false;
+                if (leader) {
+                    mbar_arrive_expect_tx(bar_kv_full + s, C::kTileBytes);
+                    for (int c = 0; c < C::kChunks; ++c)
+                        tma_load_3d(sRing + s * C::kTileBytes + c * C::kChunkBytes, map, bar_kv_full + s, 64 * c,
+                                    it.kv_head, it.kv_row + j * 128);
+                }
+                __syncwarp();
+                ++slot;
+                return true;
+            };
+            int q_loads = 0;
+            for (int k = 0; next_item(k, it); ++k) {
+                const int n = max(it.n[0], it.n[1]);
+                if (n == 0) continue;  // no row of the item sees a key
+                if (!load_kv(&tmK, 0)) break;
+                if (q_loads > 0 && !wait(bar_q_empty, (q_loads - 1) & 1)) break;
+                if (leader) {
+                    const int tiles = it.rows[1] > 0 ? 2 : 1;
+                    mbar_arrive_expect_tx(bar_q_full, tiles * C::kTileBytes);
+                    for (int t = 0; t < tiles; ++t)
+                        for (int c = 0; c < C::kChunks; ++c)
+                            tma_load_3d(sQ + t * C::kTileBytes + c * C::kChunkBytes, &tmQ, bar_q_full, 64 * c,
+                                        it.q_head[t], it.q_row[t]);
+                }
+                __syncwarp();
+                ++q_loads;
+                bool ok = load_kv(&tmV, 0);
+                for (int j = 1; ok && j < n; ++j) ok = load_kv(&tmK, j) && load_kv(&tmV, j);
+                if (!ok) break;
+            }
+            // Every copy the leader issued must land before the block exits.
+            int dummy = 0;
+            volatile int* no_abort = &dummy;
+            if (q_loads > 0)
+                mbar_wait_bounded(bar_q_full, (q_loads - 1) & 1, no_abort, status, kStatusTimeout, kTimeoutNs);
+            for (int i = max(0, slot - S); i < slot; ++i)
+                mbar_wait_bounded(bar_kv_full + i % S, (i / S) & 1, no_abort, status, kStatusTimeout, kTimeoutNs);
+            __syncwarp();
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ MMA issuer
+            const uint64_t qdesc0 = smem_desc(smem_u32(sQ), 16, 1024, kLayoutSw128);
+            const uint64_t kdesc0 = smem_desc(smem_u32(sRing), 16, 1024, kLayoutSw128);
+            // V as B operand with the channels contiguous: 64-channel chunks kChunkBytes apart, 8-key groups 1024 bytes apart
+            const uint64_t vdesc0 = smem_desc(smem_u32(sRing), C::kChunkBytes, 1024, kLayoutSw128);
+            constexpr uint32_t kIdescS = f16_idesc(128, 128, FP16, false);
+            constexpr uint32_t kIdescO = f16_idesc(128, D, FP16, true);
+            int slot = 0;            // number of the item's K(0) in the ring
+            uint32_t p_phase[2] = {0, 0};
+            Item it;
+            auto issue_s = [&](int t, int s) {
+                tc_fence_after_sync();
+                if (leader) {
+                    const uint64_t qd = qdesc0 + static_cast<uint32_t>(t * (C::kTileBytes >> 4));
+                    const uint64_t kd = kdesc0 + static_cast<uint32_t>(s * (C::kTileBytes >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2;
+                        tc_mma_f16(tbase + C::kColS + 128 * t, qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(bar_s_full + t);
+                }
+                __syncwarp();
+            };
+            auto issue_pv = [&](int t, int j, int s) {
+                tc_fence_after_sync();
+                if (leader) {
+                    const uint64_t vd = vdesc0 + static_cast<uint32_t>(s * (C::kTileBytes >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        tc_mma_f16_ts(tbase + C::kColO + D * t, tbase + C::kColS + 128 * t + 8 * kk, vd + kk * (2048 >> 4),
+                                      kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(bar_o_done + t);
+                }
+                __syncwarp();
+            };
+            auto kv_ready = [&](int i) { return wait(bar_kv_full + i % S, (i / S) & 1); };
+            int q_loads = 0;
+            for (int k = 0; next_item(k, it); ++k) {
+                const int n = max(it.n[0], it.n[1]);
+                if (n == 0) continue;
+                bool ok = wait(bar_q_full, q_loads & 1) && kv_ready(slot);
+                if (!ok) break;
+                ++q_loads;
+                for (int t = 0; t < 2; ++t)
+                    if (it.n[t] > 0) issue_s(t, slot % S);
+                if (leader) {
+                    tc_commit(bar_kv_empty + slot % S);
+                    if (n == 1) tc_commit(bar_q_empty);
+                }
+                __syncwarp();
+                for (int j = 0; ok && j < n; ++j) {
+                    const int v = slot + 2 * j + 1, kn = v + 1;
+                    ok = kv_ready(v);
+                    for (int t = 0; ok && t < 2; ++t) {
+                        if (j < it.n[t]) {
+                            ok = wait(bar_p_full + t, p_phase[t]);
+                            if (!ok) break;
+                            p_phase[t] ^= 1;
+                            issue_pv(t, j, v % S);
+                        }
+                        if (j + 1 < it.n[t]) {
+                            ok = kv_ready(kn);
+                            if (ok) issue_s(t, kn % S);
+                        }
+                    }
+                    if (ok && leader) {
+                        tc_commit(bar_kv_empty + v % S);
+                        if (j + 1 < n) tc_commit(bar_kv_empty + kn % S);
+                        if (j + 2 == n) tc_commit(bar_q_empty);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                slot += 2 * n;
+            }
+            if (leader) tc_commit(bar_drain);
+            __syncwarp();
+            int dummy = 0;
+            mbar_wait_bounded(bar_drain, 0, &dummy, status, kStatusTimeout, kTimeoutNs);
+            __syncwarp();
+        } else if (warp == 10) {
+            // ------------------------------------------------------------ scheduler
+            const PromptArgs& a = p.a;
+            const int G = a.Hq / a.Hkv;
+            int64_t before = 0;  // items of the sequences before the window
+            int b0 = -32, k = 0;
+            int64_t incl = 0, count = 0, total = 0;
+            int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+            bool more = true;
+            for (int64_t item = blockIdx.x; more; item += gridDim.x, ++k) {
+                while (b0 < 0 || (item >= before + total && b0 < a.B)) {  // next window of 32 sequences
+                    before += total;
+                    b0 += 32;
+                    const int b = b0 + lane;
+                    count = 0;
+                    if (b < a.B) {
+                        bool ok = packed_range(a.q_offsets, b, a.total_q, q0, q1);
+                        ok &= packed_range(a.kv_offsets, b, a.total_kv, k0, k1);
+                        if (!ok && blockIdx.x == 0) atomicOr(status, kStatusInvalid);
+                        const int64_t tiles = (static_cast<int64_t>(q1 - q0) + 127) / 128 * G;
+                        count = (tiles + 1) / 2 * a.Hkv;
+                    }
+                    incl = count;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o) incl += y;
+                    }
+                    total = __shfl_sync(0xffffffffu, incl, 31);
+                }
+                more = item < before + total;
+                const int64_t at = item - before;
+                const uint32_t who = __ballot_sync(0xffffffffu, at >= incl - count && at < incl);
+                const int s = k % C::kItems;
+                if (k >= C::kItems && !wait(bar_item_empty + s, ((k / C::kItems) - 1) & 1)) break;
+                if (more ? lane == __ffs(who) - 1 : lane == 0) {
+                    Item it{};
+                    it.last = more ? 0 : 1;
+                    if (more) {
+                        const int64_t r = at - (incl - count);
+                        const int64_t pair = r / a.Hkv;
+                        const int n = q1 - q0, m = k1 - k0;
+                        const int64_t F = static_cast<int64_t>((n + 127) / 128) * G;
+                        it.kv_head = static_cast<int>(r % a.Hkv);
+                        it.kv_row = k0;
+                        it.m = m;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int64_t f = F - 1 - 2 * pair - t;
+                            if (f < 0) break;
+                            const int tile = static_cast<int>(f / G);
+                            it.q_row[t] = q0 + tile * 128;
+                            it.q_head[t] = it.kv_head * G + static_cast<int>(f % G);
+                            it.rows[t] = min(128, n - tile * 128);
+                            it.lim0[t] = a.causal ? tile * 128 + 1 + m - n : m;
+                            const int seen = a.causal ? min(m, it.lim0[t] + it.rows[t] - 1) : m;
+                            it.n[t] = seen > 0 ? (seen + 127) / 128 : 0;
+                        }
+                    }
+                    items[s] = it;
+                    mbar_arrive(bar_item_full + s);
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        warpgroup_regs_inc<C::kSoftRegs>();
+        // ------------------------------------------------------------ softmax (thread = query row of tile t)
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t t_s = tbase + lane_base + C::kColS + 128 * t;
+        const uint32_t t_o = tbase + lane_base + C::kColO + D * t;
+        const float kq = p.kq;
+        int steps = 0;  // key tiles of this query tile since the start: phase of s_full and o_done
+        int slot = 0;   // as the MMA issuer's
+        Item it;
+        bool ok = true;
+        for (int k = 0; ok && next_item(k, it); ++k) {
+            const int n = it.n[t];
+            const int limit = p.a.causal ? min(it.m, it.lim0[t] + row) : it.m;  // keys this row sees
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int j = 0; j < n; ++j) {
+                if (!wait(bar_s_full + t, (steps + j) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                float sv[128];
+                {
+                    uint32_t sr[64];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        tmem_ld64_sync(t_s + 64 * c, sr);
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) sv[64 * c + i] = __uint_as_float(sr[i]);
+                    }
+                }
+                // a tile with a place that some row of the query tile does not see
+                const bool masked = (j + 1) * 128 > min(it.lim0[t], it.m);
+                if (masked) {
+                    const int seen = limit - j * 128;
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (i >= seen) sv[i] = -INFINITY;
+                }
+                float mx[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mx[c] = fmax3(sv[32 * c], sv[32 * c + 1], sv[32 * c + 2]);
+#pragma unroll
+                    for (int i = 3; i < 31; i += 2) mx[c] = fmax3(mx[c], sv[32 * c + i], sv[32 * c + i + 1]);
+                    mx[c] = fmaxf(mx[c], sv[32 * c + 31]);
+                }
+                const float m_tile = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+                // The maximum is only followed when it has grown by 2^8 (or from nothing): P <= 2^8 until then.
+                const bool grow = m_tile > m_run && (m_run == -INFINITY || (m_tile - m_run) * kq > 8.f);
+                const float m_new = grow ? m_tile : m_run;
+                const float alpha = grow ? ex2_approx((m_run - m_new) * kq) : 1.f;
+                const float bias = m_new == -INFINITY ? 0.f : -m_new * kq;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t pw[64];
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    float w0, w1, v0, v1;
+                    ffma2_bcast(w0, w1, sv[2 * i], sv[2 * i + 1], kq, bias);
+                    if (fma_pair(i % 16)) {
+                        exp2_pair(w0, w1, v0, v1);
+                    } else {
+                        v0 = ex2_approx(w0);
+                        v1 = ex2_approx(w1);
+                    }
+                    fadd2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], v0, v1);
+                    pw[i] = narrow2<FP16>(v0, v1);
+                    if (i == 31) tmem_st32(t_s, pw);
+                }
+                tmem_st32(t_s + 32, pw + 32);
+                l_run = fmaf(l_run, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                m_run = m_new;
+                if (j > 0 && __any_sync(0xffffffffu, grow)) {
+                    if (!wait(bar_o_done + t, (steps + j - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        uint32_t r[64];
+                        tmem_ld64_sync(t_o + 64 * c, r);
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) fmul2_bcast(r[i], r[i + 1], r[i], r[i + 1], alpha);
+                        tmem_st64(t_o + 64 * c, r);
+                    }
+                }
+                // V rows behind the sequence's last key: zero, so that 0 * (what they hold) is 0.
+                if ((j + 1) * 128 > it.m) {
+                    const int v = slot + 2 * j + 1;
+                    if (!wait(bar_kv_full + v % S, (v / S) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (row >= it.m - j * 128) {
+                        uint8_t* vr = sRing + (v % S) * C::kTileBytes + row * 128;
+#pragma unroll
+                        for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<uint4*>(vr + c * C::kChunkBytes + 16 * i) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_st_wait();
+                tc_fence_before_sync();
+                mbar_arrive(bar_p_full + t);
+            }
+            if (!ok) break;
+            // Epilogue: O / l.
+            const bool valid = row < it.rows[t];
+            const float inv = m_run == -INFINITY ? 0.f : 1.f / l_run;
+            uint16_t* out = p.a.o + (it.q_row[t] + row) * p.a.o_token + it.q_head[t] * p.a.o_head;
+            float* lse = p.a.lse == nullptr ? nullptr : p.a.lse + it.q_head[t] * p.a.lse_head + it.q_row[t] + row;
+            bool spoiled = false;
+            if (n > 0) {
+                if (!wait(bar_o_done + t, (steps + n - 1) & 1)) break;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32_sync(t_o + 32 * c, r);
+                    uint32_t w[16];
+                    float odd = 0.f;  // NaN if a value is infinite or NaN
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float v0 = __uint_as_float(r[2 * i]), v1 = __uint_as_float(r[2 * i + 1]);
+                        odd = fmaf(v0, 0.f, fmaf(v1, 0.f, odd));
+                        w[i] = m_run == -INFINITY ? 0u : narrow2<FP16>(v0 * inv, v1 * inv);
+                    }
+                    spoiled |= odd != 0.f;
+                    if (valid) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) =
+                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    }
+                }
+                tc_fence_before_sync();
+            } else if (valid) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(0, 0, 0, 0);
+            }
+            // m_run is in units of the raw score: ln sum = m scale + ln l = (m kq + log2 l) ln 2
+            if (valid && lse != nullptr)
+                *lse = m_run == -INFINITY ? -INFINITY : fmaf(m_run, kq, log2f(l_run)) * 0.693147180559945f;
+            // A row whose sum over V was spoiled by a place it does not see (its own weights' sum is finite).
+            uint32_t again = __ballot_sync(0xffffffffu, p.a.causal && valid && spoiled && m_run != -INFINITY &&
+                                                            l_run - l_run == 0.f);
+            __syncwarp();  // the lanes' stores above come before the warp's
+            while (again) {
+                const int who = __ffs(again) - 1;
+                again &= again - 1;
+                const int r = (warp & 3) * 32 + who;
+                const int see = min(it.m, it.lim0[t] + r);
+                attend_row<D, FP16>(p.a.q + (it.q_row[t] + r) * p.a.q_token + it.q_head[t] * p.a.q_head,
+                                    p.a.k + it.kv_row * p.a.k_token + it.kv_head * p.a.k_head,
+                                    p.a.v + it.kv_row * p.a.v_token + it.kv_head * p.a.v_head, p.a.k_token,
+                                    p.a.v_token, see, p.a.scale,
+                                    p.a.o + (it.q_row[t] + r) * p.a.o_token + it.q_head[t] * p.a.o_head, nullptr);
+            }
+            steps += n;
+            slot += 2 * max(it.n[0], it.n[1]);
+        }
+    }
+    tc_fence_before_sync();
+    named_barrier_sync(1, C::kThreads);
+    if (warp == 9) {
+        tc_fence_after_sync();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+// [rows, heads, d] 16-bit tensor, boxes of 64 channels x 1 head x 128 rows, 128-byte swizzle.
+bool encode_rows(CUtensorMap* map, const void* base, int d, int heads, int64_t rows, int64_t head_stride,
+                 int64_t row_stride, bool fp16) {
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(row_stride) * 2};
+    cuuint32_t box[3] = {64, 1, 128};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool FP16>
+cudaError_t launch_impl(const PromptArgs& a, cudaStream_t stream) {
+    using C = Cfg<D>;
+    static bool ready[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev]) {
+        // The register split takes for granted that the launch allocates exactly kLaunchRegs a thread.
+        cudaFuncAttributes fa{};
+        e = cudaFuncGetAttributes(&fa, prompt_kernel<D, FP16>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != static_cast<int>(C::kLaunchRegs)) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(prompt_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        ready[dev] = true;
+    }
+    CUtensorMap tq, tk, tv;
+    if (!encode_rows(&tq, a.q, D, a.Hq, a.total_q, a.q_head, a.q_token, FP16)) return cudaErrorInvalidValue;
+    if (a.total_kv > 0) {
+        if (!encode_rows(&tk, a.k, D, a.Hkv, a.total_kv, a.k_head, a.k_token, FP16) ||
+            !encode_rows(&tv, a.v, D, a.Hkv, a.total_kv, a.v_head, a.v_token, FP16))
+            return cudaErrorInvalidValue;
+    } else {
+        tk = tv = tq;  // never read: no item has a key
+    }
+    KParams kp{};
+    kp.a = a;
+    kp.kq = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    // At most this many items: each sequence's tiles of a group, two at a time, rounded up.
+    const int64_t G = a.Hq / a.Hkv;
+    const int64_t tiles = a.total_q / 128 + min(static_cast<int64_t>(a.B), a.total_q);
+    const int64_t most = (tiles * G + 1) / 2 * a.Hkv + static_cast<int64_t>(a.B) * a.Hkv;
+    const int grid = static_cast<int>(min(most, static_cast<int64_t>(sm_count(dev))));
+    prompt_kernel<D, FP16><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, kp);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
+int sm_count(int dev) {
+    static int count[kMaxDevices] = {};
+    if (count[dev] == 0) cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev);
+    return count[dev] > 0 ? count[dev] : 1;
+}
+
 cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t stream) {
-    if (a.total_q == 0) return cudaSuccess;
-    const dim3 grid(static_cast<unsigned>(a.total_q), (a.Hq + 3) / 4);
-    if (a.d == 128) {
-        if (a.fp16) prompt_rows_kernel<128, true><<<grid, 128, 0, stream>>>(a);
-        else prompt_rows_kernel<128, false><<<grid, 128, 0, stream>>>(a);
-    } else {
-        if (a.fp16) prompt_rows_kernel<64, true><<<grid, 128, 0, stream>>>(a);
-        else prompt_rows_kernel<64, false><<<grid, 128, 0, stream>>>(a);
-    }
-    return cudaGetLastError();
+    if (a.d == 128) return a.fp16 ? launch_impl<128, true>(a, stream) : launch_impl<128, false>(a, stream);
+    return a.fp16 ? launch_impl<64, true>(a, stream) : launch_impl<64, false>(a, stream);
 }
 
 }  // namespace mxattn

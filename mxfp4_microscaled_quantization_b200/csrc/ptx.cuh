@@ -199,6 +199,28 @@ __device__ __forceinline__ void tc_mma_nvf4(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit operands, fp32 accumulator.
+__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The same with A in TMEM: row = lane, two consecutive K elements per 32-bit column.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 #define MXATTN_R8(b) "=r"(v[b + 0]), "=r"(v[b + 1]), "=r"(v[b + 2]), "=r"(v[b + 3]), \
                      "=r"(v[b + 4]), "=r"(v[b + 5]), "=r"(v[b + 6]), "=r"(v[b + 7])
 #define MXATTN_W8(b) "r"(v[b + 0]), "r"(v[b + 1]), "r"(v[b + 2]), "r"(v[b + 3]), \
@@ -245,6 +267,15 @@ __device__ __forceinline__ void tmem_st64(uint32_t taddr, const uint32_t (&v)[64
         "%49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, %64};" ::"r"(taddr),
         MXATTN_W8(0), MXATTN_W8(8), MXATTN_W8(16), MXATTN_W8(24), MXATTN_W8(32), MXATTN_W8(40), MXATTN_W8(48),
         MXATTN_W8(56)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        MXATTN_W8(0), MXATTN_W8(8), MXATTN_W8(16), MXATTN_W8(24)
         : "memory");
 }
 
@@ -303,6 +334,17 @@ __host__ __device__ constexpr uint32_t nvf4_idesc(uint32_t n) {
            | (1u << 10)               // B format E2M1
            | ((n >> 3) << 17)         // N / 8
            | ((128u >> 4) << 24);     // M / 16
+}
+
+// Instruction descriptor of tcgen05.mma kind::f16 (fp32 accumulator): both
+// operands bf16 or both fp16, A K-major, B K-major or (b_mn) MN-major.
+__host__ __device__ constexpr uint32_t f16_idesc(uint32_t m, uint32_t n, bool fp16, bool b_mn) {
+    return (1u << 4)                          // accumulator fp32
+           | ((fp16 ? 0u : 1u) << 7)          // A format
+           | ((fp16 ? 0u : 1u) << 10)         // B format
+           | ((b_mn ? 1u : 0u) << 16)         // B major
+           | ((n >> 3) << 17)                 // N / 8
+           | ((m >> 4) << 24);                // M / 16
 }
 
 __device__ __forceinline__ float lg2_approx(float x) {

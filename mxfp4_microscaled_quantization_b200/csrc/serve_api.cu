@@ -20,8 +20,8 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 // Strides in elements of a [tokens, heads, d] tensor whose rows of d elements
 // are contiguous: 16-byte rows, and no two rows on top of each other.
 bool strides_ok(int64_t token, int64_t head, int d) {
-    return token >= d && head >= d && token % 8 == 0 && head % 8 == 0 && token < (int64_t(1) << 40) &&
-           head < (int64_t(1) << 40);
+    return token >= d && head >= d && token % 8 == 0 && head % 8 == 0 && token < (int64_t(1) << 38) &&
+           head < (int64_t(1) << 38);
 }
 
 mxattn_status check_heads(int B, int Hq, int Hkv, int d, mxattn_dtype dtype) {

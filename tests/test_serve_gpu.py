@@ -106,6 +106,10 @@ def test_prompt_strided():
     check_prompt(q, k, v, [0, 100, n], [0, 100, n], True, out=o)
     one, want = randn(g, 1, 8, d), randn(g, 1, 2, d)
     check_prompt(one, want, want, [0, 1], [0, 1], True)
+    heads_first = [randn(g, h, n, d).transpose(0, 1) for h in (8, 2, 2)]
+    check_prompt(*heads_first, [0, 200, n], [0, 200, n], True)
+    wide = [randn(g, n, h, 192)[:, :, 8:8 + d] for h in (8, 2, 2)]  # heads 192 apart
+    check_prompt(*wide, [0, 200, n], [0, 200, n], False)
 
 
 def test_prompt_rows_of_no_sequence_stay():
