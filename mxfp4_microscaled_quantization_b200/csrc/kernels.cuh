@@ -89,6 +89,7 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream);
 
 // Devices whose per-device set-up a launcher remembers, and a device's SMs.
 constexpr int kMaxDevices = 64;
+constexpr int kMaxSms = 160;  // SMs a device's workspaces are sized for (a B200 has 148)
 int sm_count(int dev);
 
 // Attention over packed prompts (16-bit operands).  Pointers and strides in

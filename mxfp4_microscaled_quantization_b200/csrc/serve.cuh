@@ -37,6 +37,32 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
     return w;
 }
 
+// Smallest e with amax <= 448 * 2^e for amax >= 0 in fp32 (448 = 1.75 * 2^8):
+// floor(log2 amax) - 8, plus one where the significand exceeds 1.75.  amax = 0
+// gives -127; fp16's subnormals are normal numbers in fp32, and bf16's end at
+// the clamp.
+__device__ __forceinline__ int e4m3_exponent(float amax) {
+    const uint32_t bits = __float_as_uint(amax);
+    const int E = static_cast<int>(bits >> 23);
+    if (E == 0) return -127;
+    const int e = E - 135 + (((bits & 0x7FFFFFu) > 0x600000u) ? 1 : 0);
+    return min(max(e, -127), 127);
+}
+
+// Two fp32 values to two E4M3 codes (lo in the low byte): nearest even, beyond
+// +-448 saturated, NaN stays NaN.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ void unpack_e4m3x2(uint32_t b, float& lo, float& hi) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(b)));
+    widen2<true>(h2, lo, hi);
+}
+
 // Sequence b's rows [begin, end) from the offsets of a packed batch.  Offsets
 // that decrease or leave [0, total] are brought into range, so no access can
 // leave the tensors, and reported.

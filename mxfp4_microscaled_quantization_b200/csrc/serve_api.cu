@@ -139,7 +139,8 @@ MXATTN_API mxattn_status mxattn_cache_attend(const void* Q, mxattn_dtype dtype, 
     if (st != MXATTN_OK) return st;
     if (num_pages < 0 || max_pages < 0 || table_stride < max_pages) return MXATTN_ERR_INVALID;
     const int shift = page_shift(page);
-    if (shift < 0 || int64_t(max_pages) * page > kMaxTokens) return MXATTN_ERR_UNSUPPORTED;
+    if (shift < 0 || int64_t(max_pages) * page > kMaxTokens || int64_t(num_pages) * Hkv >= (int64_t(1) << 31))
+        return MXATTN_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned(workspace, 256) ||
         workspace_bytes < kStatusBytes + mxattn::cache_attend_scratch_bytes(Hq, Hkv, d))
         return MXATTN_ERR_INVALID;

@@ -421,6 +421,21 @@ def test_attend_query_sizes():
     check_attend(randn(g, 1, 4, 64, dtype=FP, scale=2.0 ** -12), cache, table, [200])
 
 
+def test_attend_nan_queries_and_keys():
+    """What a sequence sees and is NaN or infinite makes its own rows NaN, no others."""
+    g = gen(27)
+    cache, table = fill(g, [200] * 4, 1, 64, 128, BF)
+    q = randn(g, 4, 8, 128)
+    want, _, to, _ = ref.attend(q, *cache, table, [200] * 4)
+    q[1, 2, 5], q[2, 3, 6] = math.nan, math.inf
+    cache[1][table[3][3], 0, 199 % 64, 9] = 0x7F
+    o, lse = mx.mxattn_cache_attend(q, *cache, i32(table), i32([200] * 4))
+    assert torch.isnan(o[1, 2]).all() and torch.isnan(o[2, 3]).all() and torch.isnan(lse[1, 2]) and torch.isnan(o[3, :, 9]).all()
+    for x in (o, want):
+        x[1, 2], x[2, 3], x[3, :, 9] = 0, 0, 0
+    ref.close(o, want, to)
+
+
 def test_attend_shared_pages_and_strides():
     g = gen(23)
     cache, table = fill(g, [640], 2, 64, 128, BF)
