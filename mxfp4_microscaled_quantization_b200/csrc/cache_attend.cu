@@ -17,11 +17,11 @@
 //     before.  A part takes 4 bits, so two hold bf16's 8 significant bits and
 //     three fp16's 11, down to 2^-10 (2^-18 of the largest element).  The
 //     parts' products add up in one accumulator.
-//   * P as p1 + p2 / 16 (+ p3 / 256), the rest scaled by 16 before it is
-//     rounded, so it does not run out of exponent:  relative error 2^-8 (bf16;
-//     bf16's own rounding) or 2^-12 (fp16), and 2^-19 (2^-23) of the largest
-//     weight where that is more.  The parts are further columns of the second
-//     product, added up in the end.
+//   * P as p1 + p2 / 16 + p3 / 256, the rest scaled by 16 before it is rounded,
+//     so it does not run out of exponent:  relative error 2^-12, or 2^-23 of a
+//     weight of 1 where that is more (a long context under one strong token has
+//     most of its weight in values of 2^-15).  The parts are further columns of
+//     the second product, added up in the end.
 // A token's K exponent scales its scores; its V exponent goes into P, relative
 // to the largest one so far.  Maxima, sums and O are fp32.
 //
@@ -60,39 +60,48 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr int kTile = 128;                      // tokens
 constexpr int kThreads = 224;
 constexpr int kCtasPerSm = 2;
-constexpr int kMaxCols = 32;                    // query heads a block handles together
+constexpr int kPairCost = 1;                    // a pair's start and end, in tiles
+constexpr int kMaxCols = 16;                    // query heads a block handles together
+constexpr int kPParts = 3;                      // E4M3 parts of P
 constexpr float kGrow = 3.f;                    // log2 of the growth of a maximum that is put up with
 constexpr float kPUnit = 32.f;                  // P's unit: 32 * 2^3 <= 448
 
-// D channels, GC query heads (1 .. GC used), PARTS E4M3 parts of Q and P.
+// D channels, GC query heads (1 .. GC used), PARTS E4M3 parts of Q.
 template <int D, int GC, int PARTS>
 struct Cfg {
-    static constexpr int NC = GC < 16 ? 16 : GC;     // columns of S^T
-    static constexpr int NO = NC * PARTS;            // columns of O^T
+    static constexpr int NC = 16;                    // columns of S^T
+    static constexpr int NO = NC * kPParts;          // columns of O^T
     static constexpr int kTileBytes = kTile * D;     // a K or V tile
     static constexpr int kQBytes = NC * D;           // one part of Q
     static constexpr int kPBytes = kTile * NO;       // P of a tile, [column chunk of 16][token][16]
-    static constexpr int kFixed = PARTS * kQBytes + 2 * kPBytes + 2048;
+    static constexpr int kFixed = PARTS * kQBytes + kPBytes + 2048;
     // 228 KB an SM, 1 KB of each block is the system's
     static constexpr int kSlots = ((228 * 1024) / kCtasPerSm - 1024 - 1024 - kFixed) / kTileBytes;
     static_assert(kSlots >= 4, "ring");
     static constexpr int kOffQ = 0;
     static constexpr int kOffRing = (kOffQ + PARTS * kQBytes + 1023) / 1024 * 1024;
-    static constexpr int kOffP = kOffRing + kSlots * kTileBytes;  // [2]
-    static constexpr int kOffMax = kOffP + 2 * kPBytes;           // float [2][NC][4], then u32 [2][4]
-    static constexpr int kOffBar = kOffMax + 2 * NC * 16 + 32;
-    // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], s_empty[2], p_full[2], pv_done[2], drain
-    static constexpr int kNumBars = 2 + 2 * kSlots + 8 + 1;
-    static constexpr int kOffCol = kOffBar + kNumBars * 8;        // float [NC]: 2^eq * scale * log2 e
-    static constexpr int kOffMisc = kOffCol + NC * 4;             // TMEM base, abort flag, run start
+    static constexpr int kOffP = kOffRing + kSlots * kTileBytes;
+    static constexpr int kOffMax = kOffP + kPBytes;               // float [NC][4], then u32 [4]
+    static constexpr int kOffBar = kOffMax + NC * 16 + 16;
+    // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], s_empty[2], p_full, pv_done, drain
+    static constexpr int kNumBars = 2 + 2 * kSlots + 4 + 2 + 1;
+    static constexpr int kOffCol = (kOffBar + kNumBars * 8 + 15) / 16 * 16;  // float [2][NC]: 2^eq * scale * log2 e
+    static constexpr int kOffBase = kOffCol + 2 * NC * 4;         // float [NC]: the maxima that P is relative to
+    // uint2 [kRing][8]: the exponents of a tile's pages, as long as its K or V tile may be in the ring
+    static constexpr int kScaleRing = kSlots / 2 + 2;
+    static constexpr int kOffScale = (kOffBase + NC * 4 + 7) / 8 * 8;
+    static constexpr int kOffMisc = kOffScale + kScaleRing * 64;  // TMEM base, abort flag
     static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
     static_assert(kSmemBytes <= 113 * 1024, "two blocks an SM");
     // TMEM: S [2][NC], O [NO]
-    static constexpr uint32_t kCols = 2 * NC + NO <= 64 ? 64 : 2 * NC + NO <= 128 ? 128 : 256;
+    static constexpr uint32_t kCols = 128;
+    static_assert(2 * NC + NO <= kCols, "TMEM");
     static_assert(kCtasPerSm * kCols <= 512, "TMEM");
     static constexpr uint32_t kLayout = D == 128 ? kLayoutSw128 : kLayoutSw64;
     static constexpr uint32_t kSbo = 8 * D;          // 8 rows of K, V or Q
-    static constexpr size_t kSlotFloats = static_cast<size_t>(GC) * (D + 1);  // workspace slot: o [GC][D], L [GC]
+    // Workspace: a slot of o [GC][D], L [GC] for each of a block's two parts, then what each block leaves to join.
+    static constexpr size_t kSlotFloats = static_cast<size_t>(GC) * (D + 1);
+    static constexpr size_t kJoinOffset = 2 * static_cast<size_t>(kMaxSms) * kCtasPerSm * kSlotFloats;  // floats
 };
 
 struct KParams {
@@ -119,7 +128,7 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// N consecutive fp32 columns of this thread's TMEM lane (N = 4, 8, 16 or 32).
+// N consecutive fp32 columns of this thread's TMEM lane (N = 4, 8 or 16).
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* v) {
 #define MXATTN_R4(b) "=r"(v[b]), "=r"(v[b + 1]), "=r"(v[b + 2]), "=r"(v[b + 3])
@@ -135,16 +144,14 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* v) {
             : MXATTN_R4(0), MXATTN_R4(4)
             : "r"(taddr)
             : "memory");
-    } else if constexpr (N == 16) {
+    } else {
+        static_assert(N == 16, "columns");
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
             "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
             : MXATTN_R4(0), MXATTN_R4(4), MXATTN_R4(8), MXATTN_R4(12)
             : "r"(taddr)
             : "memory");
-    } else {
-        tmem_ld<16>(taddr, v);
-        tmem_ld<16>(taddr + 16, v + 16);
     }
 #undef MXATTN_R4
 }
@@ -172,15 +179,32 @@ __device__ __forceinline__ float log2_to_float(uint32_t e8m0) {  // 2^(byte - 12
 // 2^-k for k >= 0; 0 where that would leave the normal numbers.
 __device__ __forceinline__ float pow2_neg(uint32_t k) { return k > 126 ? 0.f : __uint_as_float((127 - k) << 23); }
 
+// Barrier 2 of the four softmax warps: true in all of them if `x` is in any thread.
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t y;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(y)
+        : "r"(static_cast<uint32_t>(x))
+        : "memory");
+    return y != 0;
+}
+
 // A length as the kernels take it: within [0, max_pages * page].
 __device__ __forceinline__ int clean_len(const AttendArgs& a, int b) {
     return max(0, min(a.lens[b], a.max_pages << a.page_shift));
 }
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+__device__ __forceinline__ int cost_of(int len) { return len > 0 ? tiles_of(len) + kPairCost : 0; }
 
-// The list of tiles.  Position x of the list: sequences in order, each its key
-// heads' chunks in order, each its tiles in order.  `run` is called by all
+// The list of the work.  Sequences in order, each its key heads' chunks in
+// order, each (a pair) kPairCost positions for its start and end and then one for
+// each of its tiles: a run of the list is cut out by cost.  A pair's first
+// part is the one with its first tile.  `run` is called by all
 // threads of the block (blockDim.x a multiple of 32, at most 256) and gives the
 // total and, for the position `want(total)`, its sequence and the position
 // that the sequence starts at.  All threads get the same.
@@ -197,7 +221,7 @@ __device__ Where locate(const AttendArgs& a, int pairs, F want) {
     const int per = (a.B + blockDim.x - 1) / blockDim.x;
     const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
     int64_t mine = 0;
-    for (int b = lo; b < hi; ++b) mine += tiles_of(clean_len(a, b));
+    for (int b = lo; b < hi; ++b) mine += cost_of(clean_len(a, b));
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -222,7 +246,7 @@ __device__ Where locate(const AttendArgs& a, int pairs, F want) {
     if (r.at >= base && r.at < incl * pairs) {
         int b = lo;
         for (;; ++b) {
-            const int64_t n = static_cast<int64_t>(tiles_of(clean_len(a, b))) * pairs;
+            const int64_t n = static_cast<int64_t>(cost_of(clean_len(a, b))) * pairs;
             if (r.at < base + n) break;
             base += n;
         }
@@ -235,38 +259,59 @@ __device__ Where locate(const AttendArgs& a, int pairs, F want) {
     return r;
 }
 
-// Run of block c of C: positions [start(c), start(c + 1)) of the list.
-__device__ __forceinline__ int64_t run_start(int64_t total, int c, int C) { return total / C * c + total % C * c / C; }
+// a / b for a >= 0, b > 0: in 32 bits wherever a fits (a 64-bit quotient costs several times as much).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// The list cut into `count` runs: the first `more` have size + 1 positions, the others `size`.
+struct Runs {
+    int64_t size;
+    int more;
+    __device__ Runs(int64_t total, int count) : size(quotient(total, count)), more(static_cast<int>(total - size * count)) {}
+    __device__ int64_t start(int c) const { return size * c + min(c, more); }
+    __device__ int of(int64_t x) const {
+        const int64_t longer = (size + 1) * more;
+        return x < longer ? static_cast<int>(quotient(x, size + 1)) : more + static_cast<int>(quotient(x - longer, size));
+    }
+};
 
 // The pieces of a run, in order.
 struct Pieces {
     const AttendArgs& a;
     int64_t x, end, base;
-    int pairs, b, len, tiles;
+    int pairs, b, len, cost;
     // the current piece
+    int64_t from;       // its first position
     int pair, tile0, n;
     bool begins, ends;  // at the pair's first tile; behind its last
 
     __device__ Pieces(const AttendArgs& args, int pairs_, int64_t x_, int64_t end_, int64_t base_, int b_)
         : a(args), x(x_), end(end_), base(base_), pairs(pairs_), b(b_) {
         len = x < end ? clean_len(a, b) : 0;
-        tiles = tiles_of(len);
+        cost = cost_of(len);
     }
     __device__ bool next() {
-        if (x >= end) return false;
-        while (x >= base + static_cast<int64_t>(tiles) * pairs) {
-            base += static_cast<int64_t>(tiles) * pairs;
-            len = clean_len(a, ++b);
-            tiles = tiles_of(len);
+        while (x < end) {
+            while (x >= base + static_cast<int64_t>(cost) * pairs) {
+                base += static_cast<int64_t>(cost) * pairs;
+                len = clean_len(a, ++b);
+                cost = cost_of(len);
+            }
+            const int64_t off = x - base;
+            pair = static_cast<int>(quotient(off, cost));
+            const int u = static_cast<int>(off - static_cast<int64_t>(pair) * cost);
+            const int m = static_cast<int>(min(static_cast<int64_t>(cost - u), end - x));
+            from = x;
+            x += m;
+            tile0 = max(u - kPairCost, 0);
+            n = u + m - kPairCost - tile0;
+            begins = tile0 == 0;
+            ends = u + m == cost;
+            if (n > 0) return true;  // else the run ends before the pair's first tile
         }
-        const int64_t off = x - base;
-        pair = static_cast<int>(off / tiles);
-        tile0 = static_cast<int>(off - static_cast<int64_t>(pair) * tiles);
-        n = static_cast<int>(min(static_cast<int64_t>(tiles - tile0), end - x));
-        begins = tile0 == 0;
-        ends = tile0 + n == tiles;
-        x += n;
-        return true;
+        return false;
     }
 };
 
@@ -286,9 +331,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint8_t* sQ = smem + C::kOffQ;
     uint8_t* sRing = smem + C::kOffRing;
     uint8_t* sP = smem + C::kOffP;
-    float* sMax = reinterpret_cast<float*>(smem + C::kOffMax);             // [2][NC][4]
-    uint32_t* sEv = reinterpret_cast<uint32_t*>(sMax + 2 * NC * 4);        // [2][4]
-    float* sCol = reinterpret_cast<float*>(smem + C::kOffCol);             // [NC]
+    float* sMax = reinterpret_cast<float*>(smem + C::kOffMax);             // [NC][4]
+    uint32_t* sEv = reinterpret_cast<uint32_t*>(sMax + NC * 4);            // [4]
+    float* sCol = reinterpret_cast<float*>(smem + C::kOffCol);             // [2][NC]
+    float* sBase = reinterpret_cast<float*>(smem + C::kOffBase);           // [NC]
+    uint2* sScale = reinterpret_cast<uint2*>(smem + C::kOffScale);         // [kScaleRing][8]
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint64_t* bar_q_full = bars;
     uint64_t* bar_q_empty = bars + 1;
@@ -297,8 +344,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint64_t* bar_s_full = bar_kv_empty + S;
     uint64_t* bar_s_empty = bar_s_full + 2;
     uint64_t* bar_p_full = bar_s_empty + 2;
-    uint64_t* bar_pv_done = bar_p_full + 2;
-    uint64_t* bar_drain = bar_pv_done + 2;
+    uint64_t* bar_pv_done = bar_p_full + 1;
+    uint64_t* bar_drain = bar_pv_done + 1;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     const AttendArgs& a = p.a;
@@ -306,19 +353,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int P = a.page_shift, pairs = a.Hkv * p.chunks;
 
+    if (tid == 96) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmK) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmV) : "memory");
+    }
     if (tid == 0) {
         mbar_init(bar_q_full, 1);
-        mbar_init(bar_q_empty, 2);  // the products that read Q, and the softmax's reads of its scales
+        mbar_init(bar_q_empty, 2);  // the products that read Q; the softmax, which has left the piece before
         for (int s = 0; s < S; ++s) {
-            mbar_init(bar_kv_full + s, 1);
+            mbar_init(bar_kv_full + s, 2);  // the tile's bytes, its pages' exponents (K's slot; nothing more for V's)
             mbar_init(bar_kv_empty + s, 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar_s_full + s, 1);
             mbar_init(bar_s_empty + s, 128);
-            mbar_init(bar_p_full + s, 128);
-            mbar_init(bar_pv_done + s, 1);
         }
+        mbar_init(bar_p_full, 128);
+        mbar_init(bar_pv_done, 1);
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
         fence_mbarrier_init();
@@ -331,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         tmem_relinquish();
     }
     const int cta = blockIdx.x;
-    const Where at = locate(a, pairs, [&](int64_t total) { return run_start(total, cta, p.ctas); });
-    const int64_t x0 = at.at, x1 = run_start(at.total, cta + 1, p.ctas);
+    const Where at = locate(a, pairs, [&](int64_t total) { return Runs(total, p.ctas).start(cta); });
+    const int64_t x0 = at.at, x1 = Runs(at.total, p.ctas).start(cta + 1);
     // Sequences without a token, and reports of lengths out of range.
     for (int b = cta; b < a.B; b += p.ctas) {
         const int given = a.lens[b];
@@ -362,6 +413,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int ppt = kTile >> P;  // pages of a tile
         int slot = 0;
         bool ok = true;
+        // The exponents of a tile's pages follow one tile behind its copies, so their loads have time to arrive.
+        uint32_t late_ks = 0, late_vs = 0;
+        bool late_good = false;
+        auto publish = [&](int k_slot) {  // of the tile whose K is in running slot k_slot
+            if (lane < ppt)
+                sScale[k_slot / 2 % C::kScaleRing * 8 + lane] =
+                    make_uint2(__float_as_uint(log2_to_float(late_ks)), late_vs | (late_good ? 0x100u : 0u));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_kv_full + k_slot % S);
+            __syncwarp();
+        };
         while (ok && it.next()) {
             const int head = it.pair / p.chunks;
             const int used = (it.len + a.page - 1) >> P;  // pages that hold tokens
@@ -374,6 +436,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const int ahead = t + 1 < it.tile0 + it.n ? page_of(t + 1) : -2;
                 const bool good = pg >= 0 && pg < a.num_pages;
                 if (!good && pg != -2) atomicOr(status, kStatusInvalid);
+                uint32_t ks = 0, vs = 0;
+                if (good) {
+                    const int64_t cell = static_cast<int64_t>(pg) * a.Hkv + head;
+                    ks = a.k_scales[cell];
+                    vs = a.v_scales[cell];
+                }
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, good)) * (a.page * D);
                 for (int kv = 0; kv < 2; ++kv) {
                     const int s = slot % S;
@@ -381,17 +449,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         ok = false;
                         break;
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(bar_kv_full + s, bytes);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar_kv_full + s, bytes);
+                        if (kv) mbar_arrive(bar_kv_full + s);
+                    }
                     __syncwarp();
                     if (good)
                         tma_load_3d(sRing + s * C::kTileBytes + lane * a.page * D, kv ? &tmV : &tmK, bar_kv_full + s, 0, 0,
                                     pg * a.Hkv + head);
                     __syncwarp();
+                    if (kv == 0 && slot > 0) publish(slot - 2);
                     ++slot;
                 }
+                late_ks = ks;
+                late_vs = vs;
+                late_good = good;
                 pg = ahead;
             }
         }
+        if (slot > 0) publish((slot - 1) & ~1);
         // Every copy issued must land before the block exits.
         int dummy = 0;
         for (int i = max(0, slot - S); i < slot; ++i)
@@ -429,16 +505,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         };
         auto issue_pv = [&](int n, bool first) -> bool {
             const int i = 2 * n + 1, s = i % S;
-            if (!kv_ready(i) || !wait(bar_p_full + (n & 1), (n / 2) & 1)) return false;
+            if (!kv_ready(i) || !wait(bar_p_full, n & 1)) return false;
             tc_fence_after_sync();
             if (leader) {
                 const uint64_t vd = rd + static_cast<uint32_t>(s * (C::kTileBytes >> 4));
-                const uint64_t b = pd + static_cast<uint32_t>((n & 1) * (C::kPBytes >> 4));
 #pragma unroll
                 for (int kk = 0; kk < kTile / 32; ++kk)
-                    tc_mma_f8(tbase + col_o, vd + kk * ((32 * D) >> 4), b + kk * ((32 * 16) >> 4), kIdescO,
+                    tc_mma_f8(tbase + col_o, vd + kk * ((32 * D) >> 4), pd + kk * ((32 * 16) >> 4), kIdescO,
                               first && kk == 0 ? 0u : 1u);
-                tc_commit(bar_pv_done + (n & 1));
+                tc_commit(bar_pv_done);
                 tc_commit(bar_kv_empty + s);
             }
             __syncwarp();
@@ -467,50 +542,64 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int k = 0; it.next(); ++k) {
             const int head0 = it.pair / p.chunks * p.G + it.pair % p.chunks * p.per;
             const int heads = min(p.per, p.G - it.pair % p.chunks * p.per);
-            uint32_t raw[GC][E / 2];
+            constexpr int R = GC < 8 ? GC : 8;  // rows at a time; the first are ready before their place is free
+            bool ok = true;
+            for (int g0 = 0; g0 < GC; g0 += R) {
+                uint32_t raw[R][E / 2], parts[R][PARTS];
 #pragma unroll
-            for (int g = 0; g < GC; ++g)
+                for (int g = 0; g < R; ++g)
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i)
-                    raw[g][i] = g < heads ? *reinterpret_cast<const uint32_t*>(a.q + it.b * a.q_seq + (head0 + g) * a.q_head +
-                                                                               lane * E + 2 * i)
-                                          : 0u;
-            if (k > 0 && !wait(bar_q_empty, (k - 1) & 1)) break;
+                    for (int i = 0; i < E / 2; ++i)
+                        raw[g][i] = g0 + g < heads ? *reinterpret_cast<const uint32_t*>(
+                                                         a.q + it.b * a.q_seq + (head0 + g0 + g) * a.q_head + lane * E + 2 * i)
+                                                   : 0u;
+                float my_col = 0.f;  // lane g: row g's factor
 #pragma unroll
-            for (int g = 0; g < GC; ++g) {
-                float x[E], top = 0.f;
+                for (int g = 0; g < R; ++g) {
+                    float x[E], top = 0.f;
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i) {
-                    widen2<FP16>(raw[g][i], x[2 * i], x[2 * i + 1]);
-                    top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
-                }
-                top = redux_max(top);
-                const int e = e4m3_exponent(top);
-                // an infinite query has no finite parts: NaN, as its products with the keys are
-                const float down = isinf(top) ? NAN : exp2_neg_int(e);
-#pragma unroll
-                for (int i = 0; i < E; ++i) x[i] *= down;
-                if (lane == 0) sCol[g] = log2_to_float(e + 127) * p.kq;
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part) {
-                    uint32_t w = 0;
-#pragma unroll
-                    for (int i = 0; i < E; i += 2) {
-                        const uint32_t c = pack_e4m3x2(x[i], x[i + 1]);
-                        float v0, v1;
-                        unpack_e4m3x2(c, v0, v1);
-                        x[i] -= v0;
-                        x[i + 1] -= v1;
-                        w |= c << (8 * i);
+                    for (int i = 0; i < E / 2; ++i) {
+                        widen2<FP16>(raw[g][i], x[2 * i], x[2 * i + 1]);
+                        top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
                     }
+                    top = redux_max(top);
+                    const int e = e4m3_exponent(top);
+                    // an infinite query has no finite parts: NaN, as its products with the keys are
+                    const float down = isinf(top) ? NAN : exp2_neg_int(e);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) x[i] *= down;
+                    if (lane == g) my_col = log2_to_float(e + 127) * p.kq;
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) {
+                        parts[g][part] = 0;
+#pragma unroll
+                        for (int i = 0; i < E; i += 2) {
+                            const uint32_t c = pack_e4m3x2(x[i], x[i + 1]);
+                            float v0, v1;
+                            unpack_e4m3x2(c, v0, v1);
+                            x[i] -= v0;
+                            x[i + 1] -= v1;
+                            parts[g][part] |= c << (8 * i);
+                        }
+                    }
+                }
+                if (g0 == 0 && k > 0) ok = wait(bar_q_empty, (k - 1) & 1);
+                if (!ok) break;
+                if (lane < R) sCol[(k & 1) * NC + g0 + lane] = my_col;
+#pragma unroll
+                for (int g = 0; g < R; ++g) {
                     // swizzled like a TMA tile of D-byte rows
-                    const int byte = lane * E;
-                    const int chunk = D == 128 ? (byte >> 4) ^ (g & 7) : (byte >> 4) ^ ((g >> 1) & 3);
-                    uint8_t* at8 = sQ + part * C::kQBytes + g * D + chunk * 16 + (byte & 15);
-                    if constexpr (E == 4) *reinterpret_cast<uint32_t*>(at8) = w;
-                    else *reinterpret_cast<uint16_t*>(at8) = static_cast<uint16_t>(w);
+                    const int byte = lane * E, row = g0 + g;
+                    const int chunk = D == 128 ? (byte >> 4) ^ (row & 7) : (byte >> 4) ^ ((row >> 1) & 3);
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) {
+                        uint8_t* at8 = sQ + part * C::kQBytes + row * D + chunk * 16 + (byte & 15);
+                        if constexpr (E == 4) *reinterpret_cast<uint32_t*>(at8) = parts[g][part];
+                        else *reinterpret_cast<uint16_t*>(at8) = static_cast<uint16_t>(parts[g][part]);
+                    }
                 }
             }
+            if (!ok) break;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_q_full);
@@ -522,91 +611,88 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
         const uint32_t t_o = tbase + lane_base + col_o;
         int n = 0;
+        int4 to_join = make_int4(-1, 0, 0, 0);  // sequence, first head, heads and slot, last block with a part
         for (int k = 0; it.next(); ++k) {
             const int chunk = it.pair % p.chunks, head = it.pair / p.chunks;
             const int head0 = head * p.G + chunk * p.per, heads = min(p.per, p.G - chunk * p.per);
             const int last = it.tile0 + it.n;
-            // The token's page two tiles ahead, its page's exponents one ahead.
-            auto page_of = [&](int tile) {
-                const int token = tile * kTile + tid;
-                return tile < last && token < it.len ? page_at(a, it.b, token >> P) : -1;
-            };
-            auto scales_of = [&](int pg) -> uint32_t {  // K's exponent byte, V's << 8, bit 16: valid
-                if (pg < 0 || pg >= a.num_pages) return 0;
-                const int64_t cell = static_cast<int64_t>(pg) * a.Hkv + head;
-                return a.k_scales[cell] | a.v_scales[cell] << 8 | 1u << 16;
-            };
-            uint32_t sc = scales_of(page_of(it.tile0));
-            int pg1 = page_of(it.tile0 + 1);
-            float m[GC], l[GC], col[GC];
-            uint32_t ev = 0;  // largest exponent of V so far
             wait(bar_q_full, k & 1);
-#pragma unroll
-            for (int g = 0; g < GC; ++g) {
-                m[g] = -INFINITY;
-                l[g] = 0.f;
-                col[g] = sCol[g];
-            }
-            named_barrier_sync(2, 128);  // all have read sCol
             if (tid == 0) mbar_arrive(bar_q_empty);
+            const float4* col = reinterpret_cast<const float4*>(sCol + (k & 1) * NC);
+            const float4* base4 = reinterpret_cast<const float4*>(sBase);
+            float l[GC];
+#pragma unroll
+            for (int g = 0; g < GC; ++g) l[g] = 0.f;
+            uint32_t ev = 0;    // largest exponent of V so far
+            bool fresh = true;  // no token so far
             for (int t = it.tile0; t < last; ++t, ++n) {
-                const uint32_t sc1 = scales_of(pg1);
-                const int pg2 = page_of(t + 2);
                 wait(bar_s_full + (n & 1), (n / 2) & 1);
                 tc_fence_after_sync();
-                float s[GC];
+                float w[GC];  // log2 of the weights, relative to the bases
                 {
                     uint32_t r[GC];
                     tmem_ld<GC>(tbase + lane_base + (n & 1) * NC, r);
 #pragma unroll
-                    for (int g = 0; g < GC; ++g) s[g] = __uint_as_float(r[g]);
+                    for (int g = 0; g < GC; ++g) w[g] = __uint_as_float(r[g]);
                 }
                 tc_fence_before_sync();
                 mbar_arrive(bar_s_empty + (n & 1));
-                const bool valid = sc >> 16;
-                const float ks = log2_to_float(sc & 0xFFu);
-                const uint32_t my_ev = (sc >> 8) & 0xFFu;
-                float* mx = sMax + (n & 1) * NC * 4;
-                float keep = 0.f;
+                // S is there, so its K tile's barrier has completed: the exponents are too
+                const uint2 sc = sScale[n % C::kScaleRing * 8 + (tid >> P)];
+                const bool valid = t * kTile + tid < it.len && sc.y >= 0x100u;
+                const float ks = __uint_as_float(sc.x);
+                const uint32_t my_ev = sc.y & 0xFFu;
+                float over = -INFINITY;
 #pragma unroll
-                for (int g = 0; g < GC; ++g) {
-                    s[g] = valid ? s[g] * (ks * col[g]) : -INFINITY;
-                    const float top = redux_max(s[g]);
-                    if (lane == g) keep = top;
-                }
-                if (lane < GC) mx[lane * 4 + warp] = keep;
-                const uint32_t top_ev = __reduce_max_sync(0xffffffffu, valid ? my_ev : 0u);
-                if (lane == 0) sEv[(n & 1) * 4 + warp] = top_ev;
-                named_barrier_sync(2, 128);
-                const uint4 e4 = *reinterpret_cast<const uint4*>(sEv + (n & 1) * 4);
-                const uint32_t ev_tile = max(max(e4.x, e4.y), max(e4.z, e4.w));
-                const bool first = t == it.tile0;
-                bool grown = first || ev_tile > ev;
-                float m_tile[GC];
+                for (int q = 0; q < GC / 4; ++q) {
+                    const float4 c4 = col[q], b4 = base4[q];
+                    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-                for (int g = 0; g < GC; ++g) {
-                    const float4 v = *reinterpret_cast<const float4*>(mx + g * 4);
-                    m_tile[g] = fmaxf(fmax3(v.x, v.y, v.z), v.w);
-                    grown |= m_tile[g] > m[g] + kGrow || (m[g] == -INFINITY && m_tile[g] > -INFINITY);
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = fmaf(w[4 * q + i], ks * c[i], fresh ? 0.f : -b[i]);
+                        w[4 * q + i] = valid ? x : -INFINITY;
+                    }
+                    over = fmaxf(fmax3(over, w[4 * q], w[4 * q + 1]), fmaxf(w[4 * q + 2], w[4 * q + 3]));
                 }
-                // P's buffer: PV(n - 2) has read it
-                if (n >= 2) wait(bar_pv_done + (n & 1), (n / 2 - 1) & 1);
-                if (grown) {  // the same in every thread
-                    const uint32_t ev_new = first ? ev_tile : max(ev, ev_tile);
-                    const float f = first ? 1.f : pow2_neg(ev_new - ev);
+                const bool grow = softmax_any(fresh || over > kGrow || (valid && my_ev > ev));
+                if (grow) {  // the same in every thread
+                    const bool first = t == it.tile0;
+                    float keep = 0.f;
+#pragma unroll
+                    for (int g = 0; g < GC; ++g) {
+                        const float top = redux_max(w[g]);
+                        if (lane == g) keep = top;
+                    }
+                    if (lane < GC) sMax[lane * 4 + warp] = keep;
+                    const uint32_t top_ev = __reduce_max_sync(0xffffffffu, valid ? my_ev + 1 : 0u);
+                    if (lane == 0) sEv[warp] = top_ev;
+                    named_barrier_sync(2, 128);
+                    const uint4 e4 = *reinterpret_cast<const uint4*>(sEv);
+                    const uint32_t ev_tile = max(max(e4.x, e4.y), max(e4.z, e4.w));  // 1 more than the exponent; 0: no token
+                    const uint32_t ev_new = max(ev, max(ev_tile, 1u) - 1);
+                    const float f = pow2_neg(ev_new - ev);
+                    // Lane g: how far head g's base moves (to the maximum if this is the first, or if it has grown by
+                    // 2^kGrow) and what that makes of what has been summed up.
+                    float move = 0.f;
+                    if (lane < GC) {
+                        const float4 v = *reinterpret_cast<const float4*>(sMax + lane * 4);
+                        const float top = fmaxf(fmax3(v.x, v.y, v.z), v.w);
+                        if (fresh ? top != -INFINITY : top > kGrow) move = top;
+                        if (warp == 0) sBase[lane] = fresh ? move : sBase[lane] + move;
+                    }
+                    const float scale = fresh ? 0.f : ex2_approx(-move);
                     float alpha[GC];
 #pragma unroll
                     for (int g = 0; g < GC; ++g) {
-                        const bool up = m_tile[g] > m[g] + kGrow || (m[g] == -INFINITY && m_tile[g] > -INFINITY);
-                        const float m_new = up ? m_tile[g] : m[g];
-                        alpha[g] = up ? ex2_approx(m[g] - m_new) : 1.f;
+                        w[g] -= __shfl_sync(0xffffffffu, move, g);
+                        alpha[g] = __shfl_sync(0xffffffffu, scale, g);
                         l[g] *= alpha[g];
                         alpha[g] *= f;
-                        m[g] = m_new;
                     }
+                    fresh = ev_tile == 0 && fresh;
                     ev = ev_new;
                     if (!first) {
-                        wait(bar_pv_done + ((n - 1) & 1), ((n - 1) / 2) & 1);
+                        wait(bar_pv_done, (n - 1) & 1);
                         tc_fence_after_sync();
 #pragma unroll
                         for (int c = 0; c < C::NO / 16; ++c) {
@@ -621,36 +707,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         }
                         tmem_st_wait();
                     }
+                    named_barrier_sync(2, 128);  // the bases are written before the next tile reads them
                 }
                 // P in units of 2^ev: weights times 2^(own exponent - ev) * 32
                 const float vf = valid ? pow2_neg(ev - my_ev) * kPUnit : 0.f;
-                uint8_t* pb = sP + (n & 1) * C::kPBytes + tid * 16;
+                uint8_t* pb = sP + tid * 16;
 #pragma unroll
                 for (int c = 0; c < NC / 16; ++c) {
-                    uint32_t w[PARTS][4];
+                    uint32_t pw[kPParts][4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
+                        if (16 * c + 4 * q >= GC) {
+#pragma unroll
+                            for (int part = 0; part < kPParts; ++part) pw[part][q] = 0;
+                            continue;
+                        }
                         float x[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int g = 16 * c + 4 * q + i;
-                            if (g < GC) {
-                                const float pr = ex2_approx(s[g < GC ? g : 0] - (m[g < GC ? g : 0] == -INFINITY ? 0.f : m[g < GC ? g : 0]));
-                                l[g < GC ? g : 0] += pr;
-                                x[i] = pr * vf;
-                            } else {
-                                x[i] = 0.f;
-                            }
+                            const int g = (16 * c + 4 * q + i) % GC;
+                            const float pr = ex2_approx(w[g]);
+                            l[g] += pr;
+                            x[i] = pr * vf;
                         }
 #pragma unroll
-                        for (int part = 0; part < PARTS; ++part) {
-                            if (16 * c + 4 * q >= GC) {
-                                w[part][q] = 0;
-                                continue;
-                            }
+                        for (int part = 0; part < kPParts; ++part) {
                             const uint32_t lo = pack_e4m3x2(x[0], x[1]), hi = pack_e4m3x2(x[2], x[3]);
-                            w[part][q] = lo | hi << 16;
-                            if (part + 1 < PARTS) {
+                            pw[part][q] = lo | hi << 16;
+                            if (part + 1 < kPParts) {
                                 float v[4];
                                 unpack_e4m3x2(lo, v[0], v[1]);
                                 unpack_e4m3x2(hi, v[2], v[3]);
@@ -659,10 +743,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             }
                         }
                     }
+                    if (n > 0) wait(bar_pv_done, (n - 1) & 1);  // PV(n - 1) has read the buffer
 #pragma unroll
-                    for (int part = 0; part < PARTS; ++part)
+                    for (int part = 0; part < kPParts; ++part)
                         *reinterpret_cast<uint4*>(pb + (part * (NC / 16) + c) * (kTile * 16)) =
-                            make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]);
+                            make_uint4(pw[part][0], pw[part][1], pw[part][2], pw[part][3]);
                 }
                 // V rows of no token: zero, so that 0 * (what they hold) is 0.
                 if (__any_sync(0xffffffffu, !valid)) {
@@ -676,12 +761,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
-                mbar_arrive(bar_p_full + (n & 1));
-                sc = sc1;
-                pg1 = pg2;
+                mbar_arrive(bar_p_full);
             }
             // End of the piece: the row sums over the tile's threads, then O^T / l.
-            float* sum = sMax + (n & 1) * NC * 4;  // free until the next tile's maxima
+            float* sum = sMax;  // free: the last maxima have been read
             float keep = 0.f;
 #pragma unroll
             for (int g = 0; g < GC; ++g) {
@@ -689,45 +772,55 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 if (lane == g) keep = v;
             }
             if (lane < GC) sum[lane * 4 + warp] = keep;
-            wait(bar_pv_done + ((n - 1) & 1), ((n - 1) / 2) & 1);
+            wait(bar_pv_done, (n - 1) & 1);
             tc_fence_after_sync();
             named_barrier_sync(2, 128);
             float o[GC];
 #pragma unroll
-            for (int part = PARTS - 1; part >= 0; --part) {
+            for (int part = kPParts - 1; part >= 0; --part) {
                 uint32_t r[GC];
                 tmem_ld<GC>(t_o + part * NC, r);
 #pragma unroll
                 for (int g = 0; g < GC; ++g)
-                    o[g] = part == PARTS - 1 ? __uint_as_float(r[g]) : fmaf(o[g], 1.f / 16.f, __uint_as_float(r[g]));
+                    o[g] = part == kPParts - 1 ? __uint_as_float(r[g]) : fmaf(o[g], 1.f / 16.f, __uint_as_float(r[g]));
             }
             tc_fence_before_sync();
-            const float unit = log2_to_float(ev) * (1.f / kPUnit);
+            // Lane g: head g's sum of weights, what O is multiplied by, and log2 of the sum.
+            float by = 0.f, L = -INFINITY;
+            if (lane < GC) {
+                const float4 v = *reinterpret_cast<const float4*>(sum + lane * 4);
+                const float lt = (v.x + v.y) + (v.z + v.w);
+                if (lt != 0.f) {  // 0: every token left out
+                    by = log2_to_float(ev) * (1.f / kPUnit) * (1.f / lt);
+                    L = sBase[lane] + log2f(lt);
+                }
+            }
             // lane -> channel: 128 rows lie in all lanes, 64 in the first 16 of each warp
             const int ch = D == 128 ? tid : warp * 16 + lane;
             const bool mine = D == 128 || lane < 16;
-            const bool whole = it.begins && it.ends;
-            float* slot = reinterpret_cast<float*>(a.scratch) + (2 * static_cast<size_t>(cta) + (it.x - it.n == x0 ? 0 : 1)) * C::kSlotFloats;
 #pragma unroll
-            for (int g = 0; g < GC; ++g) {
-                const float4 v = *reinterpret_cast<const float4*>(sum + g * 4);
-                const float lt = (v.x + v.y) + (v.z + v.w);
-                const bool none = lt == 0.f;  // every token left out
-                const float val = none ? 0.f : o[g] * (1.f / lt) * unit;
-                const float L = none ? -INFINITY : m[g] + log2f(lt);  // log2 of the sum of weights
-                if (g < heads) {
-                    if (whole) {
-                        if (mine) a.o[it.b * a.o_seq + (head0 + g) * a.o_head + ch] = static_cast<uint16_t>(narrow2<FP16>(val, 0.f));
-                        if (a.lse != nullptr && tid == g)
-                            a.lse[static_cast<int64_t>(it.b) * a.Hq + head0 + g] = L * 0.693147180559945f;
-                    } else {
-                        if (mine) slot[g * D + ch] = val;
-                        if (tid == g) slot[GC * D + g] = L;
-                    }
-                }
+            for (int g = 0; g < GC; ++g) o[g] *= __shfl_sync(0xffffffffu, by, g);
+            if (it.begins && it.ends) {
+                uint16_t* out = a.o + it.b * a.o_seq + head0 * a.o_head + ch;
+#pragma unroll
+                for (int g = 0; g < GC; ++g)
+                    if (mine && g < heads) out[g * a.o_head] = static_cast<uint16_t>(narrow2<FP16>(o[g], 0.f));
+                if (a.lse != nullptr && tid < heads)
+                    a.lse[static_cast<int64_t>(it.b) * a.Hq + head0 + tid] = L * 0.693147180559945f;
+            } else {
+                float* slot = reinterpret_cast<float*>(a.scratch) +
+                              (2 * static_cast<size_t>(cta) + (it.from == x0 ? 0 : 1)) * C::kSlotFloats;
+#pragma unroll
+                for (int g = 0; g < GC; ++g)
+                    if (mine) slot[g * D + ch] = o[g];
+                if (tid < GC) slot[GC * D + tid] = L;
+                // The block with a pair's first tile leaves the join to the kernel behind this one.
+                if (it.begins) to_join = make_int4(it.b, head0, heads | (it.from == x0 ? 0 : 1 << 16),
+                                                   Runs(at.total, p.ctas).of(it.base + static_cast<int64_t>(it.pair + 1) * it.cost - 1));
             }
-            named_barrier_sync(2, 128);  // the sums are read before the next piece writes maxima there
+            named_barrier_sync(2, 128);  // the sums and bases are read before the next piece writes there
         }
+        if (tid == 0) reinterpret_cast<int4*>(reinterpret_cast<float*>(a.scratch) + C::kJoinOffset)[cta] = to_join;
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -739,50 +832,61 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 // Joins the parts of the pairs that several blocks had, in the order of the
 // list: o = sum_c w_c o_c / sum_c w_c, w_c = 2^(L_c - max L).  Block c takes the
-// pair that begins in run c and goes on behind it, if there is one; a warp a
-// head, D / 32 channels a lane.
+// pair that begins in run c and goes on behind it, if there is one: four blocks,
+// a quarter of the heads each, whose warps share out heads and parts (four,
+// because one alone takes 8 us for a pair of 74 parts with 8 heads, a block a
+// head costs more in blocks with nothing to do).
+constexpr int kJoinWarps = 8, kJoinSplit = 4;
 template <int D, bool FP16, int GC>
-__global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ KParams p) {
-    constexpr int E = D / 32;
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const __grid_constant__ KParams p) {
+    constexpr int E = D / 32, kHeads = GC / kJoinSplit, kShares = kJoinWarps / kHeads;  // heads of a block, warps of a head
     using C = Cfg<D, GC, FP16 ? 3 : 2>;
+    __shared__ __align__(16) float s_o[kJoinWarps][D];
+    __shared__ float s_w[kJoinWarps], s_top[kJoinWarps];
     const AttendArgs& a = p.a;
-    const int cta = blockIdx.x, pairs = a.Hkv * p.chunks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Where at = locate(a, pairs, [&](int64_t total) { return run_start(total, cta + 1, p.ctas) - 1; });
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t lo = run_start(at.total, cta, p.ctas), hi = at.at + 1;
-    if (hi <= lo) return;
-    const int tiles = tiles_of(clean_len(a, at.b));
-    const int pair = static_cast<int>((at.at - at.base) / tiles);
-    const int64_t first = at.base + static_cast<int64_t>(pair) * tiles, end = first + tiles;
-    if (end == hi || first < lo) return;  // ends here, or began before
-    int c1 = cta + 1;
-    while (run_start(at.total, c1 + 1, p.ctas) < end) ++c1;  // the last run with a part
-    const int head = pair / p.chunks, chunk = pair % p.chunks;
-    const int head0 = head * p.G + chunk * p.per, heads = min(p.per, p.G - chunk * p.per);
+    const int cta = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, share = warp % kShares;
+    const int g0 = blockIdx.y * kHeads, g = g0 + warp / kShares;
     const float* slots = reinterpret_cast<const float*>(a.scratch);
-    auto slot_of = [&](int c) { return slots + (2 * static_cast<size_t>(c) + (c == cta && first > lo ? 1 : 0)) * C::kSlotFloats; };
-    for (int g = warp; g < heads; g += 8) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 job = reinterpret_cast<const int4*>(slots + C::kJoinOffset)[cta];
+    if (job.x < 0) return;
+    const int heads = job.z & 0xFFFF, c1 = job.w;
+    auto slot_of = [&](int c) { return slots + (2 * static_cast<size_t>(c) + (c == cta ? job.z >> 16 : 0)) * C::kSlotFloats; };
+    if (g < heads) {
         float top = -INFINITY;
-        for (int c = cta + lane; c <= c1; c += 32)
-            if (run_start(at.total, c, p.ctas) < run_start(at.total, c + 1, p.ctas)) top = fmaxf(top, slot_of(c)[GC * D + g]);
+        for (int c = cta + lane; c <= c1; c += 32) top = fmaxf(top, slot_of(c)[GC * D + g]);
         top = warp_max(top);
         const float base = top == -INFINITY ? 0.f : top;
         float acc[E] = {}, total = 0.f;
-        for (int c = cta; c <= c1; ++c) {
-            if (run_start(at.total, c, p.ctas) == run_start(at.total, c + 1, p.ctas)) continue;  // an empty run
+#pragma unroll 8
+        for (int c = cta + share; c <= c1; c += kShares) {
             const float* slot = slot_of(c);
             const float w = exp2f(slot[GC * D + g] - base);
             total += w;
 #pragma unroll
             for (int i = 0; i < E; ++i) acc[i] = fmaf(w, slot[g * D + lane * E + i], acc[i]);
         }
-        const float inv = total == 0.f ? 0.f : 1.f / total;  // 0: every part's tokens were left out
-        uint16_t* out = a.o + at.b * a.o_seq + (head0 + g) * a.o_head + lane * E;
 #pragma unroll
-        for (int i = 0; i < E; i += 2) *reinterpret_cast<uint32_t*>(out + i) = narrow2<FP16>(acc[i] * inv, acc[i + 1] * inv);
-        if (a.lse != nullptr && lane == 0)
-            a.lse[static_cast<int64_t>(at.b) * a.Hq + head0 + g] =
-                (base + log2f(total)) * 0.693147180559945f;
+        for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = acc[i];
+        if (lane == 0) {
+            s_w[warp] = total;
+            s_top[warp] = base;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < min(kHeads, heads - g0) * (D / 2); i += kJoinWarps * 32) {
+        const int h = i / (D / 2), ch = i % (D / 2) * 2;
+        float o0 = 0.f, o1 = 0.f, total = 0.f;
+#pragma unroll
+        for (int w = h * kShares; w < (h + 1) * kShares; ++w) {
+            o0 += s_o[w][ch];
+            o1 += s_o[w][ch + 1];
+            total += s_w[w];
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;  // 0: every part's tokens were left out
+        *reinterpret_cast<uint32_t*>(a.o + job.x * a.o_seq + (job.y + g0 + h) * a.o_head + ch) = narrow2<FP16>(o0 * inv, o1 * inv);
+        if (ch == 0 && a.lse != nullptr)
+            a.lse[static_cast<int64_t>(job.x) * a.Hq + job.y + g0 + h] = (s_top[h * kShares] + log2f(total)) * 0.693147180559945f;
     }
 }
 
@@ -829,8 +933,8 @@ cudaError_t launch_impl(const AttendArgs& a, int dev, int G, int chunks, int per
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.ctas);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(p.ctas, kJoinSplit);
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -845,17 +949,16 @@ cudaError_t launch_heads(const AttendArgs& a, int dev, cudaStream_t stream) {
     const int G = a.Hq / a.Hkv, chunks = (G + kMaxCols - 1) / kMaxCols, per = (G + chunks - 1) / chunks;
     if (per <= 4) return launch_impl<D, FP16, 4>(a, dev, G, chunks, per, stream);
     if (per <= 8) return launch_impl<D, FP16, 8>(a, dev, G, chunks, per, stream);
-    if (per <= 16) return launch_impl<D, FP16, 16>(a, dev, G, chunks, per, stream);
-    return launch_impl<D, FP16, 32>(a, dev, G, chunks, per, stream);
+    return launch_impl<D, FP16, 16>(a, dev, G, chunks, per, stream);
 }
 
 }  // namespace
 
-// Two slots a block, each with a part's O and log-sums of up to kMaxCols heads.
+// Two slots a block, each with a part's O and log-sums of up to kMaxCols heads, and what it leaves to join.
 size_t cache_attend_scratch_bytes(int Hq, int Hkv, int d) {
     const int G = Hq / Hkv, chunks = (G + kMaxCols - 1) / kMaxCols, per = (G + chunks - 1) / chunks;
-    const size_t gc = per <= 4 ? 4 : per <= 8 ? 8 : per <= 16 ? 16 : 32;
-    return 2 * static_cast<size_t>(kMaxSms) * kCtasPerSm * gc * (d + 1) * sizeof(float);
+    const size_t gc = per <= 4 ? 4 : per <= 8 ? 8 : 16;
+    return static_cast<size_t>(kMaxSms) * kCtasPerSm * (2 * gc * (d + 1) * sizeof(float) + sizeof(int4));
 }
 
 cudaError_t launch_cache_attend(const AttendArgs& a, cudaStream_t stream) {
