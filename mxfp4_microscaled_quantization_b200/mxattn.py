@@ -507,42 +507,76 @@ def mxattn_nvfp4_attend(workspace, B, H, N, d, kv_tile=128, pnq=True, softmax_sc
 # ---------------------------------------------------------------- serving operators
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_I64x4, _I64x8 = ctypes.c_int64 * 4, ctypes.c_int64 * 8
+_attend_workspace = {}  # (Hq, Hkv, d) -> bytes
 
-
-def _rows(name, t, heads, d, dtype, device):
-    """Check a [rows, heads, d] tensor with contiguous rows; its (row, head) strides."""
-    if t.dtype != dtype or t.device != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be {dtype} [rows, {heads}, {d}] on {device}, got {t.dtype} {tuple(t.shape)} on "
-                         f"{t.device}")
-    row, head, one = t.stride()
-    if one != 1 and d != 1:
-        raise ValueError(f"{name}'s rows of {d} elements must be contiguous")
-    # a dimension of one element has no stride of its own
-    return (row if t.shape[0] > 1 else max(row, heads * d)), (head if heads > 1 else d)
-
-
-def _dense(name, t, dtype, device, numel=None, shape=None):
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}, got {t.dtype} on {t.device}")
-    if (numel is not None and t.numel() != numel) or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape if shape is not None else numel}")
-    return t.data_ptr()
+# The calls below stand between a decode step's kernels of a few microseconds, so their checks touch each tensor once:
+# a device is compared by its index, and strides are only collected where a tensor is not dense.
 
 
 def _serve_head(name, t):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{name} must be a CUDA tensor [rows, heads, d]")
-    if t.dtype not in DTYPES:
+    dt = DTYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    return DTYPES[t.dtype]
+    return dt
 
 
-def _on(device, stream, call):
-    """Run `call(stream)` with `device` current, on `stream` or the device's current stream."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return call(_stream(torch.cuda.current_stream(device) if stream is None else stream))
-    return call(_stream(stream))
+def _rows(name, t, rows, heads, d, like):
+    """Check a [rows, heads, d] tensor with contiguous rows of d elements; None if it is dense, else its (row, head)
+    strides."""
+    if t.dtype is not like.dtype or t.get_device() != like.get_device() or t.shape != (rows, heads, d):
+        raise ValueError(f"{name} must be {like.dtype} {(rows, heads, d)} on {like.device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return None
+    row, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}'s rows of {d} elements must be contiguous")
+    # a dimension of one element has no stride of its own
+    return (row if rows > 1 else max(row, heads * d)), (head if heads > 1 else d)
+
+
+def _strides(array, shapes, strides):
+    """A C array of the tensors' strides, or None where all are dense."""
+    if not any(strides):
+        return None
+    flat = []
+    for (heads, d), s in zip(shapes, strides):
+        flat += s or (heads * d, d)
+    return array(*flat)
+
+
+def _dense(name, t, dtype, like, shape):
+    if t.dtype is not dtype or t.get_device() != like.get_device() or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {like.device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _workspace(t, like):
+    if t.dtype is not torch.uint8 or t.get_device() != like.get_device() or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {like.device}")
+    return t.data_ptr()
+
+
+def _serve(fn, where, like, stream, *args):
+    """Call `fn` with `like`'s device current, on `stream` or that device's current stream."""
+    index = like.get_device()
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    else:
+        stream = int(stream)
+    if index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != 0:
+        raise MxattnError(status, where)
 
 
 def new_prompt_workspace(device="cuda") -> torch.Tensor:
@@ -564,44 +598,43 @@ def mxattn_prompt(q, k, v, q_offsets, kv_offsets=None, causal=True, softmax_scal
                   workspace=None, stream=None):
     """Attention over packed prompts: q [total_q, Hq, d], k, v [total_kv, Hkv, d] (bfloat16 or float16, strided rows),
     int32 device offsets [B + 1] (kv_offsets: the keys' where they differ) -> (out like q, lse fp32 [Hq, total_q]).
-    Rows of `out` and `lse` that belong to no sequence are left as they were."""
-    dt, dev = _serve_head("q", q), q.device
+    Rows of `out` and `lse` that belong to no sequence are left as they were (0 and -inf where the call makes them)."""
+    dt = _serve_head("q", q)
     Tq, Hq, d = q.shape
     Tk, Hkv = k.shape[0], k.shape[1]
     if out is None:
-        out = torch.zeros((Tq, Hq, d), dtype=q.dtype, device=dev)
+        out = torch.zeros((Tq, Hq, d), dtype=q.dtype, device=q.device)
     if lse is None:
-        lse = torch.full((Hq, Tq), float("-inf"), dtype=torch.float32, device=dev)
-    if kv_offsets is None:
-        kv_offsets = q_offsets
+        lse = torch.full((Hq, Tq), float("-inf"), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(256, dtype=torch.uint8, device=dev)
-    strides = (ctypes.c_int64 * 8)(*_rows("q", q, Hq, d, q.dtype, dev), *_rows("k", k, Hkv, d, q.dtype, dev),
-                                   *_rows("v", v, Hkv, d, q.dtype, dev), *_rows("out", out, Hq, d, q.dtype, dev))
-    if v.shape[0] != Tk or out.shape[0] != Tq:
-        raise ValueError("k and v, and q and out, must have the same rows")
-    B = q_offsets.numel() - 1
-    qo, ko = _dense("q_offsets", q_offsets, torch.int32, dev), _dense("kv_offsets", kv_offsets, torch.int32, dev, B + 1)
-    lp = _dense("lse", lse, torch.float32, dev, shape=(Hq, Tq))
-    wp = _dense("workspace", workspace, torch.uint8, dev)
-    _check(_on(dev, stream, lambda s: lib().mxattn_prompt(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, qo, ko, B, Tq, Tk, Hq, Hkv, d, strides, 1 if causal else 0,
-        softmax_scale, out.data_ptr(), lp, Tq, wp, workspace.numel(), s)), "mxattn_prompt")
+        workspace = torch.empty(256, dtype=torch.uint8, device=q.device)
+    strides = _strides(_I64x8, ((Hq, d), (Hkv, d), (Hkv, d), (Hq, d)),
+                       (_rows("q", q, Tq, Hq, d, q), _rows("k", k, Tk, Hkv, d, q), _rows("v", v, Tk, Hkv, d, q),
+                        _rows("out", out, Tq, Hq, d, q)))
+    n = q_offsets.shape
+    qo = ko = _dense("q_offsets", q_offsets, torch.int32, q, n)
+    if kv_offsets is not None:
+        ko = _dense("kv_offsets", kv_offsets, torch.int32, q, n)
+    _serve(lib().mxattn_prompt, "mxattn_prompt", q, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, qo, ko,
+           q_offsets.numel() - 1, Tq, Tk, Hq, Hkv, d, strides, 1 if causal else 0, softmax_scale, out.data_ptr(),
+           _dense("lse", lse, torch.float32, q, (Hq, Tq)), Tq, _workspace(workspace, q), workspace.numel())
     return out, lse
 
 
-def _cache(k_codes, v_codes, k_scales, v_scales, block_table, dev, B):
-    if k_codes.dim() != 4 or block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("the codes must be [pages, Hkv, page, d] and block_table [B, pages of a sequence]")
-    pages, Hkv, page, d = shape = tuple(k_codes.shape)
-    ptrs = (_dense("k_codes", k_codes, torch.uint8, dev), _dense("v_codes", v_codes, torch.uint8, dev, shape=shape),
-            _dense("k_scales", k_scales, torch.uint8, dev, shape=shape[:2]),
-            _dense("v_scales", v_scales, torch.uint8, dev, shape=shape[:2]))
-    if block_table.dtype != torch.int32 or block_table.device != dev or (block_table.shape[1] > 1
-                                                                         and block_table.stride(1) != 1):
-        raise ValueError(f"block_table must be int32 on {dev} with contiguous rows")
-    most = block_table.shape[1]
-    return ptrs, pages, Hkv, page, d, block_table.data_ptr(), (block_table.stride(0) if B > 1 else most), most
+def _cache(k_codes, v_codes, k_scales, v_scales, block_table, like, B):
+    """Check a cache and its block table; (code and scale pointers), pages, Hkv, page, d, (table pointer, stride, pages)."""
+    shape = k_codes.shape
+    if len(shape) != 4:
+        raise ValueError(f"k_codes must be [pages, Hkv, page, d], got {tuple(shape)}")
+    pages, Hkv, page, d = shape
+    cells = (pages, Hkv)
+    ptrs = (_dense("k_codes", k_codes, torch.uint8, like, shape), _dense("v_codes", v_codes, torch.uint8, like, shape),
+            _dense("k_scales", k_scales, torch.uint8, like, cells), _dense("v_scales", v_scales, torch.uint8, like, cells))
+    most = block_table.shape[-1]
+    if block_table.dtype is not torch.int32 or block_table.get_device() != like.get_device() or block_table.shape != (
+            B, most) or (most > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be int32 [{B}, pages of a sequence] on {like.device} with contiguous rows")
+    return ptrs, pages, Hkv, page, d, (block_table.data_ptr(), block_table.stride(0) if B > 1 else most, most)
 
 
 def new_cache(pages: int, Hkv: int, page: int, d: int, device="cuda"):
@@ -613,42 +646,37 @@ def new_cache(pages: int, Hkv: int, page: int, d: int, device="cuda"):
 def mxattn_cache_store(k, v, k_codes, v_codes, k_scales, v_scales, block_table, offsets, held_lens, status=None,
                        stream=None):
     """Store new tokens in the 8-bit paged cache: k, v [tokens, Hkv, d], sequence b's rows offsets[b] .. offsets[b + 1]
-    behind the held_lens[b] tokens it has.  `status`: optional device int32 [1] (or a workspace's first word)."""
-    dt, dev = _serve_head("k", k), k.device
-    B = held_lens.numel()
-    ptrs, pages, Hkv, page, d, tp, ts, most = _cache(k_codes, v_codes, k_scales, v_scales, block_table, dev, B)
-    strides = (ctypes.c_int64 * 4)(*_rows("k", k, Hkv, d, k.dtype, dev), *_rows("v", v, Hkv, d, k.dtype, dev))
-    if v.shape[0] != k.shape[0]:
-        raise ValueError("k and v must have the same rows")
-    op, hp = _dense("offsets", offsets, torch.int32, dev, B + 1), _dense("held_lens", held_lens, torch.int32, dev)
-    sp = None if status is None else _dense("status", status, torch.int32, dev)
-    _check(_on(dev, stream, lambda s: lib().mxattn_cache_store(
-        k.data_ptr(), v.data_ptr(), dt, k.shape[0], op, hp, B, Hkv, d, strides, *ptrs, pages, page, tp, ts, most, sp,
-        s)), "mxattn_cache_store")
+    behind the held_lens[b] tokens it has.  `status`: optional device int32 [1] that errors are ORed into."""
+    dt = _serve_head("k", k)
+    B, T = held_lens.numel(), k.shape[0]
+    ptrs, pages, Hkv, page, d, table = _cache(k_codes, v_codes, k_scales, v_scales, block_table, k, B)
+    strides = _strides(_I64x4, ((Hkv, d), (Hkv, d)), (_rows("k", k, T, Hkv, d, k), _rows("v", v, T, Hkv, d, k)))
+    _serve(lib().mxattn_cache_store, "mxattn_cache_store", k, stream, k.data_ptr(), v.data_ptr(), dt, T,
+           _dense("offsets", offsets, torch.int32, k, (B + 1,)), _dense("held_lens", held_lens, torch.int32, k, (B,)), B,
+           Hkv, d, strides, *ptrs, pages, page, *table,
+           None if status is None else _dense("status", status, torch.int32, k, (1,)))
 
 
 def mxattn_cache_attend(q, k_codes, v_codes, k_scales, v_scales, block_table, lens, softmax_scale=0.0, out=None,
                         lse=None, workspace=None, stream=None):
     """Single-token attention over the 8-bit paged cache: q [B, Hq, d] (bfloat16 or float16), int32 device lens [B]
     -> (out like q, lse fp32 [B, Hq])."""
-    dt, dev = _serve_head("q", q), q.device
+    dt = _serve_head("q", q)
     B, Hq, d = q.shape
-    ptrs, pages, Hkv, page, dc, tp, ts, most = _cache(k_codes, v_codes, k_scales, v_scales, block_table, dev, B)
+    ptrs, pages, Hkv, page, dc, table = _cache(k_codes, v_codes, k_scales, v_scales, block_table, q, B)
     if dc != d:
         raise ValueError(f"q has {d} channels, the cache {dc}")
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=q.dtype, device=dev)
+        out = torch.empty((B, Hq, d), dtype=q.dtype, device=q.device)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(lib().mxattn_cache_attend_workspace_size(Hq, Hkv, d), dtype=torch.uint8, device=dev)
-    strides = (ctypes.c_int64 * 4)(*_rows("q", q, Hq, d, q.dtype, dev), *_rows("out", out, Hq, d, q.dtype, dev))
-    if out.shape[0] != B:
-        raise ValueError("q and out must have the same rows")
-    np_ = _dense("lens", lens, torch.int32, dev, B)
-    lp = _dense("lse", lse, torch.float32, dev, shape=(B, Hq))
-    wp = _dense("workspace", workspace, torch.uint8, dev)
-    _check(_on(dev, stream, lambda s: lib().mxattn_cache_attend(
-        q.data_ptr(), dt, B, Hq, Hkv, d, strides, *ptrs, pages, page, tp, ts, most, np_, softmax_scale, out.data_ptr(),
-        lp, wp, workspace.numel(), s)), "mxattn_cache_attend")
+        need = _attend_workspace.get((Hq, Hkv, d))
+        if need is None:
+            need = _attend_workspace[Hq, Hkv, d] = int(lib().mxattn_cache_attend_workspace_size(Hq, Hkv, d))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    strides = _strides(_I64x4, ((Hq, d), (Hq, d)), (_rows("q", q, B, Hq, d, q), _rows("out", out, B, Hq, d, q)))
+    _serve(lib().mxattn_cache_attend, "mxattn_cache_attend", q, stream, q.data_ptr(), dt, B, Hq, Hkv, d, strides, *ptrs,
+           pages, page, *table, _dense("lens", lens, torch.int32, q, (B,)), softmax_scale, out.data_ptr(),
+           _dense("lse", lse, torch.float32, q, (B, Hq)), _workspace(workspace, q), workspace.numel())
     return out, lse
