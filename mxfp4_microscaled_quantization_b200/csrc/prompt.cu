@@ -14,17 +14,21 @@
 // two read the same K and V tiles whatever the group's size.  The grid is
 // persistent; block c takes the items c, c + grid, ....  Roles (384 threads):
 //   warps 0-3 / 4-7  softmax of tile A / B, a thread per query row (= TMEM
-//                    lane): the row of S from TMEM, running maximum, P back
-//                    into S's own columns in 16 bits, O rescaled in TMEM only
-//                    when the maximum has grown by more than 2^8, O / l.
+//                    lane), 64 keys a step: the row of S from TMEM, running
+//                    maximum, P back into S's own columns in 16 bits, O rescaled
+//                    in TMEM only when the maximum has grown by more than 2^8, and
+//                    in the end O / l.
 //   warp 8           TMA producer: K and V tiles of 128 keys through one ring
 //                    (K0, V0, K1, ...), Q once an item.
-//   warp 9           MMA issuer: S_t(j) = Q_t K(j)^T and O_t += P_t(j) V(j) in the
-//                    order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1): while one tile's
-//                    softmax runs, the tensor core has the other's two products.
-//                    One thread issues all of them, so the tensor core runs them
-//                    in this order, and S_t(j+1) may overwrite the columns that
-//                    PV_t(j) reads P from.
+//   warps 9 / 11     MMA issuers of tile A / B, one thread each: S_t(i) = Q_t K(i)^T
+//                    and O_t += P_t(i) V(i), a step i of 64 keys at a time, in the
+//                    order PV_t(i), S_t(i+2).  Each tile has two S buffers of 64
+//                    columns: S(i+1) is there when the softmax is done with step i.
+//                    The tensor core runs a thread's products in their order, so
+//                    S_t(i+2) may overwrite the columns that PV_t(i) reads P from.
+//                    Two issuers, because the some hundred cycles of waits and
+//                    set-up between two steps of one are covered by the other's
+//                    products (with one issuer the tensor core idled half the time).
 //   warp 10          scheduler: finds each item's sequence from the offsets (a
 //                    scan that only moves forward) and publishes the item.
 //
@@ -62,7 +66,7 @@ struct Item {
     int q_row[2];   // first row of Q and O of tile A, B
     int q_head[2];
     int rows[2];    // rows of the tile that belong to the sequence (0: no tile B)
-    int n[2];       // key tiles the tile needs
+    int n[2];       // steps of 64 keys the tile needs
     int lim0[2];    // keys that the tile's first row sees (may be <= 0)
     int kv_row, kv_head;
     int m;          // keys of the sequence
@@ -85,14 +89,14 @@ struct Cfg {
     static constexpr int kOffRing = kOffQ + 2 * kTileBytes;
     static constexpr int kOffItems = kOffRing + kSlots * kTileBytes;
     static constexpr int kOffBar = kOffItems + kItems * sizeof(Item);
-    // q_full, q_empty, kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2], o_done[2], item_full[kItems],
+    // q_full, q_empty, kv_full[kSlots], kv_empty[kSlots], s_full[2][2], p_full[2][2], o_done[2][2], item_full[kItems],
     // item_empty[kItems], drain
-    static constexpr int kNumBars = 2 + 2 * kSlots + 6 + 2 * kItems + 1;
+    static constexpr int kNumBars = 2 + 2 * kSlots + 12 + 2 * kItems + 1;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-    // TMEM columns: S (and P) of A and B, O of A and B
-    static constexpr uint32_t kColS = 0, kColO = 256;  // + 128 t, + D t
+    // TMEM columns: S (and P) of A and B, two buffers each, O of A and B
+    static constexpr uint32_t kColS = 0, kColO = 256;  // + 128 t + 64 buffer, + D t
 };
 
 struct KParams {
@@ -149,6 +153,11 @@ __device__ __forceinline__ void fadd2(float& o0, float& o1, float a0, float a1) 
         : "f"(o0), "f"(o1), "f"(a0), "f"(a1));
 }
 
+// A bounded wait after a first look has failed.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+    return mbar_wait_bounded(bar, parity, abort_flag, status, kStatusTimeout, kTimeoutNs);
+}
+
 template <int D, bool FP16>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -166,9 +175,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     uint64_t* bar_kv_full = bars + 2;
     uint64_t* bar_kv_empty = bar_kv_full + S;
     uint64_t* bar_s_full = bar_kv_empty + S;
-    uint64_t* bar_p_full = bar_s_full + 2;
-    uint64_t* bar_o_done = bar_p_full + 2;
-    uint64_t* bar_item_full = bar_o_done + 2;
+    uint64_t* bar_p_full = bar_s_full + 4;
+    uint64_t* bar_o_done = bar_p_full + 4;
+    uint64_t* bar_item_full = bar_o_done + 4;
     uint64_t* bar_item_empty = bar_item_full + C::kItems;
     uint64_t* bar_drain = bar_item_empty + C::kItems;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
@@ -178,21 +187,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         mbar_init(bar_q_full, 1);
-        mbar_init(bar_q_empty, 1);
+        mbar_init(bar_q_empty, 2);
         for (int s = 0; s < S; ++s) {
             mbar_init(bar_kv_full + s, 1);
-            mbar_init(bar_kv_empty + s, 1);
+            mbar_init(bar_kv_empty + s, 2);  // both MMA issuers
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(bar_s_full + t, 1);
-            mbar_init(bar_p_full + t, 128);
-            mbar_init(bar_o_done + t, 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(bar_s_full + 2 * t + b, 1);
+                mbar_init(bar_p_full + 2 * t + b, 128);
+                mbar_init(bar_o_done + 2 * t + b, 1);
+            }
         }
         for (int s = 0; s < C::kItems; ++s) {
             mbar_init(bar_item_full + s, 1);
-            mbar_init(bar_item_empty + s, 10);  // producer, MMA issuer, 8 softmax warps
+            mbar_init(bar_item_empty + s, 11);  // producer, MMA issuers, 8 softmax warps
         }
-        mbar_init(bar_drain, 1);
+        mbar_init(bar_drain, 2);
         *abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             };
             int q_loads = 0;
             for (int k = 0; next_item(k, it); ++k) {
-                const int n = max(it.n[0], it.n[1]);
+                const int n = (max(it.n[0], it.n[1]) + 1) / 2;  // tiles of 128 keys
                 if (n == 0) continue;  // no row of the item sees a key
                 if (!load_kv(&tmK, 0)) break;
                 if (q_loads > 0 && !wait(bar_q_empty, (q_loads - 1) & 1)) break;
@@ -267,84 +278,105 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             for (int i = max(0, slot - S); i < slot; ++i)
                 mbar_wait_bounded(bar_kv_full + i % S, (i / S) & 1, no_abort, status, kStatusTimeout, kTimeoutNs);
             __syncwarp();
-        } else if (warp == 9) {
-            // ------------------------------------------------------------ MMA issuer
-            const uint64_t qdesc0 = smem_desc(smem_u32(sQ), 16, 1024, kLayoutSw128);
-            const uint64_t kdesc0 = smem_desc(smem_u32(sRing), 16, 1024, kLayoutSw128);
-            // V as B operand with the channels contiguous: 64-channel chunks kChunkBytes apart, 8-key groups 1024 bytes apart
-            const uint64_t vdesc0 = smem_desc(smem_u32(sRing), C::kChunkBytes, 1024, kLayoutSw128);
-            constexpr uint32_t kIdescS = f16_idesc(128, 128, FP16, false);
-            constexpr uint32_t kIdescO = f16_idesc(128, D, FP16, true);
-            int slot = 0;            // number of the item's K(0) in the ring
-            uint32_t p_phase[2] = {0, 0};
-            Item it;
-            auto issue_s = [&](int t, int s) {
-                tc_fence_after_sync();
-                if (leader) {
-                    const uint64_t qd = qdesc0 + static_cast<uint32_t>(t * (C::kTileBytes >> 4));
-                    const uint64_t kd = kdesc0 + static_cast<uint32_t>(s * (C::kTileBytes >> 4));
+        } else if (warp == 9 || warp == 11) {
+            // ------------------------------------------------------------ MMA issuer of tile t: one thread
+            if (leader) {
+                const int t = warp == 9 ? 0 : 1;
+                auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
+                    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status);
+                };
+                const uint64_t qd = smem_desc(smem_u32(sQ + t * C::kTileBytes), 16, 1024, kLayoutSw128);
+                const uint64_t kd0 = smem_desc(smem_u32(sRing), 16, 1024, kLayoutSw128);
+                // V as B operand with the channels contiguous: 64-channel chunks kChunkBytes apart, 8-key groups 1024
+                const uint64_t vd0 = smem_desc(smem_u32(sRing), C::kChunkBytes, 1024, kLayoutSw128);
+                constexpr uint32_t kIdescS = f16_idesc(128, 64, FP16, false);
+                constexpr uint32_t kIdescO = f16_idesc(128, D, FP16, true);
+                const uint32_t t_s = tbase + C::kColS + 128 * t, t_o = tbase + C::kColO + D * t;
+                // Ring places and phases of the next K and V tile; steps so far (buffers and phases of S, P and O).
+                int kp = 0, vp = 1, u_s = 0, u_p = 0;
+                uint32_t kf = 0, vf = 0;
+                auto next_tile = [](int& at, uint32_t& phase) {
+                    at += 2;
+                    if (at >= S) {
+                        at -= S;
+                        phase ^= 1;
+                    }
+                };
+                // S(i), the given half of the current K tile
+                auto issue_s = [&](int half) {
+                    const uint64_t kd = kd0 + static_cast<uint32_t>(kp * (C::kTileBytes >> 4) + half * (64 * 128 >> 4));
+                    const uint32_t d = t_s + 64 * (u_s & 1);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk / 4) * (C::kChunkBytes >> 4) + (kk % 4) * 2;
-                        tc_mma_f16(tbase + C::kColS + 128 * t, qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
+                        tc_mma_f16(d, qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
                     }
-                    tc_commit(bar_s_full + t);
-                }
-                __syncwarp();
-            };
-            auto issue_pv = [&](int t, int j, int s) {
-                tc_fence_after_sync();
-                if (leader) {
-                    const uint64_t vd = vdesc0 + static_cast<uint32_t>(s * (C::kTileBytes >> 4));
+                    tc_commit(bar_s_full + 2 * t + (u_s & 1));
+                    ++u_s;
+                };
+                int q_loads = 0;
+                bool ok = true;
+                for (int k = 0; ok; ++k) {
+                    const int slot = k % C::kItems;
+                    if (!ready(bar_item_full + slot, (k / C::kItems) & 1)) break;
+                    const int n = items[slot].n[t], most = max(items[slot].n[0], items[slot].n[1]);
+                    const bool last = items[slot].last != 0;
+                    mbar_arrive(bar_item_empty + slot);
+                    if (last) break;
+                    if (most == 0) continue;
+                    ok = ready(bar_q_full, q_loads++ & 1);
+                    if (ok && n > 0) {
+                        ok = ready(bar_kv_full + kp, kf);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        issue_s(0);
+                        if (n > 1) issue_s(1);
+                        tc_commit(bar_kv_empty + kp);
+                        next_tile(kp, kf);
+                        if (n <= 2) tc_commit(bar_q_empty);
+                    }
+                    for (int i = 0; ok && i < n; ++i) {
+                        const int half = i & 1;
+                        ok = (half || ready(bar_kv_full + vp, vf)) && ready(bar_p_full + 2 * t + (u_p & 1), (u_p >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        const uint64_t vd = vd0 + static_cast<uint32_t>(vp * (C::kTileBytes >> 4) + half * (64 * 128 >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        tc_mma_f16_ts(tbase + C::kColO + D * t, tbase + C::kColS + 128 * t + 8 * kk, vd + kk * (2048 >> 4),
-                                      kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-                    tc_commit(bar_o_done + t);
-                }
-                __syncwarp();
-            };
-            auto kv_ready = [&](int i) { return wait(bar_kv_full + i % S, (i / S) & 1); };
-            int q_loads = 0;
-            for (int k = 0; next_item(k, it); ++k) {
-                const int n = max(it.n[0], it.n[1]);
-                if (n == 0) continue;
-                bool ok = wait(bar_q_full, q_loads & 1) && kv_ready(slot);
-                if (!ok) break;
-                ++q_loads;
-                for (int t = 0; t < 2; ++t)
-                    if (it.n[t] > 0) issue_s(t, slot % S);
-                if (leader) {
-                    tc_commit(bar_kv_empty + slot % S);
-                    if (n == 1) tc_commit(bar_q_empty);
-                }
-                __syncwarp();
-                for (int j = 0; ok && j < n; ++j) {
-                    const int v = slot + 2 * j + 1, kn = v + 1;
-                    ok = kv_ready(v);
-                    for (int t = 0; ok && t < 2; ++t) {
-                        if (j < it.n[t]) {
-                            ok = wait(bar_p_full + t, p_phase[t]);
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_f16_ts(t_o, t_s + 64 * (u_p & 1) + 8 * kk, vd + kk * (2048 >> 4), kIdescO,
+                                          (i > 0 || kk > 0) ? 1u : 0u);
+                        tc_commit(bar_o_done + 2 * t + (u_p & 1));
+                        ++u_p;
+                        if (half || i == n - 1) {
+                            tc_commit(bar_kv_empty + vp);
+                            next_tile(vp, vf);
+                        }
+                        if (i + 2 < n) {
+                            if (!half) ok = ready(bar_kv_full + kp, kf);
                             if (!ok) break;
-                            p_phase[t] ^= 1;
-                            issue_pv(t, j, v % S);
-                        }
-                        if (j + 1 < it.n[t]) {
-                            ok = kv_ready(kn);
-                            if (ok) issue_s(t, kn % S);
+                            tc_fence_after_sync();
+                            issue_s(half);
+                            if (half || i + 2 == n - 1) {
+                                tc_commit(bar_kv_empty + kp);
+                                next_tile(kp, kf);
+                                if (i + 2 == n - 1) tc_commit(bar_q_empty);
+                            }
                         }
                     }
-                    if (ok && leader) {
-                        tc_commit(bar_kv_empty + v % S);
-                        if (j + 1 < n) tc_commit(bar_kv_empty + kn % S);
-                        if (j + 2 == n) tc_commit(bar_q_empty);
+                    // Tiles that only the other query tile needs: given back when they are there (a place given back
+                    // before would be counted for the tile before).
+                    if (ok && n == 0) mbar_arrive(bar_q_empty);
+                    for (int j = (n + 1) / 2; ok && j < (most + 1) / 2; ++j) {
+                        ok = ready(bar_kv_full + kp, kf);
+                        if (ok) mbar_arrive(bar_kv_empty + kp);
+                        next_tile(kp, kf);
+                        ok = ok && ready(bar_kv_full + vp, vf);
+                        if (ok) mbar_arrive(bar_kv_empty + vp);
+                        next_tile(vp, vf);
                     }
-                    __syncwarp();
                 }
-                if (!ok) break;
-                slot += 2 * n;
+                tc_commit(bar_drain);
             }
-            if (leader) tc_commit(bar_drain);
             __syncwarp();
             int dummy = 0;
             mbar_wait_bounded(bar_drain, 0, &dummy, status, kStatusTimeout, kTimeoutNs);
@@ -405,7 +437,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                             it.rows[t] = min(128, n - tile * 128);
                             it.lim0[t] = a.causal ? tile * 128 + 1 + m - n : m;
                             const int seen = a.causal ? min(m, it.lim0[t] + it.rows[t] - 1) : m;
-                            it.n[t] = seen > 0 ? (seen + 127) / 128 : 0;
+                            it.n[t] = seen > 0 ? (seen + 63) / 64 : 0;
                         }
                     }
                     items[s] = it;
@@ -422,45 +454,43 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const uint32_t t_s = tbase + lane_base + C::kColS + 128 * t;
         const uint32_t t_o = tbase + lane_base + C::kColO + D * t;
         const float kq = p.kq;
-        int steps = 0;  // key tiles of this query tile since the start: phase of s_full and o_done
-        int slot = 0;   // as the MMA issuer's
+        int steps = 0;  // of this query tile before the item: buffers and phases, as the MMA issuer's
+        int slot = 0;
         Item it;
         bool ok = true;
         for (int k = 0; ok && next_item(k, it); ++k) {
             const int n = it.n[t];
             const int limit = p.a.causal ? min(it.m, it.lim0[t] + row) : it.m;  // keys this row sees
+            const int all_see = min(it.lim0[t], it.m);                          // keys that every row of the tile sees
             float m_run = -INFINITY, l_run = 0.f;
-            for (int j = 0; j < n; ++j) {
-                if (!wait(bar_s_full + t, (steps + j) & 1)) {
+            for (int i = 0; i < n; ++i) {
+                const int u = steps + i;
+                const uint32_t t_p = t_s + 64 * (u & 1);
+                if (!wait(bar_s_full + 2 * t + (u & 1), (u >> 1) & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
-                float sv[128];
+                float sv[64];
                 {
                     uint32_t sr[64];
+                    tmem_ld64_sync(t_p, sr);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        tmem_ld64_sync(t_s + 64 * c, sr);
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) sv[64 * c + i] = __uint_as_float(sr[i]);
-                    }
+                    for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(sr[c]);
                 }
-                // a tile with a place that some row of the query tile does not see
-                const bool masked = (j + 1) * 128 > min(it.lim0[t], it.m);
-                if (masked) {
-                    const int seen = limit - j * 128;
+                if ((i + 1) * 64 > all_see) {
+                    const int seen = limit - i * 64;
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (i >= seen) sv[i] = -INFINITY;
+                    for (int c = 0; c < 64; ++c)
+                        if (c >= seen) sv[c] = -INFINITY;
                 }
                 float mx[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    mx[c] = fmax3(sv[32 * c], sv[32 * c + 1], sv[32 * c + 2]);
+                    mx[c] = fmax3(sv[16 * c], sv[16 * c + 1], sv[16 * c + 2]);
 #pragma unroll
-                    for (int i = 3; i < 31; i += 2) mx[c] = fmax3(mx[c], sv[32 * c + i], sv[32 * c + i + 1]);
-                    mx[c] = fmaxf(mx[c], sv[32 * c + 31]);
+                    for (int e = 3; e < 15; e += 2) mx[c] = fmax3(mx[c], sv[16 * c + e], sv[16 * c + e + 1]);
+                    mx[c] = fmaxf(mx[c], sv[16 * c + 15]);
                 }
                 const float m_tile = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
                 // The maximum is only followed when it has grown by 2^8 (or from nothing): P <= 2^8 until then.
@@ -469,26 +499,25 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 const float alpha = grow ? ex2_approx((m_run - m_new) * kq) : 1.f;
                 const float bias = m_new == -INFINITY ? 0.f : -m_new * kq;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t pw[64];
+                uint32_t pw[32];
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
+                for (int c = 0; c < 32; ++c) {
                     float w0, w1, v0, v1;
-                    ffma2_bcast(w0, w1, sv[2 * i], sv[2 * i + 1], kq, bias);
-                    if (fma_pair(i % 16)) {
+                    ffma2_bcast(w0, w1, sv[2 * c], sv[2 * c + 1], kq, bias);
+                    if (fma_pair(c % 16)) {
                         exp2_pair(w0, w1, v0, v1);
                     } else {
                         v0 = ex2_approx(w0);
                         v1 = ex2_approx(w1);
                     }
-                    fadd2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], v0, v1);
-                    pw[i] = narrow2<FP16>(v0, v1);
-                    if (i == 31) tmem_st32(t_s, pw);
+                    fadd2(sum[2 * (c & 1)], sum[2 * (c & 1) + 1], v0, v1);
+                    pw[c] = narrow2<FP16>(v0, v1);
                 }
-                tmem_st32(t_s + 32, pw + 32);
+                tmem_st32(t_p, pw);
                 l_run = fmaf(l_run, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
                 m_run = m_new;
-                if (j > 0 && __any_sync(0xffffffffu, grow)) {
-                    if (!wait(bar_o_done + t, (steps + j - 1) & 1)) {
+                if (i > 0 && __any_sync(0xffffffffu, grow)) {
+                    if (!wait(bar_o_done + 2 * t + ((u - 1) & 1), ((u - 1) >> 1) & 1)) {
                         ok = false;
                         break;
                     }
@@ -498,30 +527,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         uint32_t r[64];
                         tmem_ld64_sync(t_o + 64 * c, r);
 #pragma unroll
-                        for (int i = 0; i < 64; i += 2) fmul2_bcast(r[i], r[i + 1], r[i], r[i + 1], alpha);
+                        for (int e = 0; e < 64; e += 2) fmul2_bcast(r[e], r[e + 1], r[e], r[e + 1], alpha);
                         tmem_st64(t_o + 64 * c, r);
                     }
                 }
                 // V rows behind the sequence's last key: zero, so that 0 * (what they hold) is 0.
-                if ((j + 1) * 128 > it.m) {
-                    const int v = slot + 2 * j + 1;
+                if ((i & 1) == 0 && i * 64 + 128 > it.m) {
+                    const int v = slot + i + 1;
                     if (!wait(bar_kv_full + v % S, (v / S) & 1)) {
                         ok = false;
                         break;
                     }
-                    if (row >= it.m - j * 128) {
+                    if (row >= it.m - i * 64) {
                         uint8_t* vr = sRing + (v % S) * C::kTileBytes + row * 128;
 #pragma unroll
                         for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<uint4*>(vr + c * C::kChunkBytes + 16 * i) = make_uint4(0, 0, 0, 0);
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4*>(vr + c * C::kChunkBytes + 16 * e) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
                 tmem_st_wait();
                 tc_fence_before_sync();
-                mbar_arrive(bar_p_full + t);
+                mbar_arrive(bar_p_full + 2 * t + (u & 1));
             }
             if (!ok) break;
             // Epilogue: O / l.
@@ -531,7 +560,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             float* lse = p.a.lse == nullptr ? nullptr : p.a.lse + it.q_head[t] * p.a.lse_head + it.q_row[t] + row;
             bool spoiled = false;
             if (n > 0) {
-                if (!wait(bar_o_done + t, (steps + n - 1) & 1)) break;
+                const int u = steps + n - 1;
+                if (!wait(bar_o_done + 2 * t + (u & 1), (u >> 1) & 1)) break;
                 tc_fence_after_sync();
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -577,7 +607,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                                     p.a.o + (it.q_row[t] + r) * p.a.o_token + it.q_head[t] * p.a.o_head, nullptr);
             }
             steps += n;
-            slot += 2 * max(it.n[0], it.n[1]);
+            slot += (max(it.n[0], it.n[1]) + 1) / 2 * 2;
         }
     }
     tc_fence_before_sync();
