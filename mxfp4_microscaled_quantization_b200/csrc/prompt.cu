@@ -12,7 +12,11 @@
 // group's Hq / Hkv heads are numbered token block first, head second, from the
 // last block down (the most keys first), and an item takes two in a row, so the
 // two read the same K and V tiles whatever the group's size.  The grid is
-// persistent; block c takes the items c, c + grid, ....  Roles (384 threads):
+// persistent.  The items of all sequences are ordered by the power of two below
+// their number of steps, the longest first, and taken as blocks become free (a
+// counter in the workspace): a ragged batch of 12 sequences ends within 2 % of an
+// even share, where every grid-th item to each block left a third of the time to
+// the slowest.  Roles (384 threads):
 //   warps 0-3 / 4-7  softmax of tile A / B, a thread per query row (= TMEM
 //                    lane), 64 keys a step: the row of S from TMEM, running
 //                    maximum, P back into S's own columns in 16 bits, O rescaled
@@ -29,8 +33,8 @@
 //                    Two issuers, because the some hundred cycles of waits and
 //                    set-up between two steps of one are covered by the other's
 //                    products (with one issuer the tensor core idled half the time).
-//   warp 10          scheduler: finds each item's sequence from the offsets (a
-//                    scan that only moves forward) and publishes the item.
+//   warp 10          scheduler: takes the next item, finds it from the offsets (a
+//                    scan that only moves forward) and publishes it.
 //
 // Masked places.  Scores of keys that a row does not see are replaced, so K may
 // hold anything there.  V rows behind the sequence's last key are zeroed in
@@ -60,6 +64,7 @@ namespace mxattn {
 namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
+constexpr int kCounterWord = 16;                // of the workspace: the counter of items (the status is word 0)
 
 // One item, as the scheduler publishes it.
 struct Item {
@@ -79,7 +84,8 @@ struct Cfg {
     static constexpr int kChunks = D / 64;                  // 128-byte column chunks of a 16-bit row
     static constexpr int kTileBytes = 128 * D * 2;          // a Q, K or V tile
     static constexpr int kChunkBytes = 128 * 128;
-    static constexpr int kSlots = 160 * 1024 / kTileBytes;  // ring of K and V tiles
+    static constexpr int kSlots = 128 * 1024 / kTileBytes;  // ring of K and V tiles
+    static constexpr int kStageBytes = 32 * 128;            // of a softmax warp: 32 rows of O, 64 channels
     static constexpr int kItems = 2;
     static constexpr int kThreads = 384;
     // 384 x 168 registers at launch; softmax warpgroups 224, the other 56 (2 x 128 x 224 + 128 x 56 == 384 x 168).
@@ -87,7 +93,8 @@ struct Cfg {
     static_assert(2 * 128 * kSoftRegs + 128 * kRoleRegs == kThreads * kLaunchRegs, "register split");
     static constexpr int kOffQ = 0;  // [2]
     static constexpr int kOffRing = kOffQ + 2 * kTileBytes;
-    static constexpr int kOffItems = kOffRing + kSlots * kTileBytes;
+    static constexpr int kOffStage = kOffRing + kSlots * kTileBytes;  // [8]
+    static constexpr int kOffItems = kOffStage + 8 * kStageBytes;
     static constexpr int kOffBar = kOffItems + kItems * sizeof(Item);
     // q_full, q_empty, kv_full[kSlots], kv_empty[kSlots], s_full[2][2], p_full[2][2], o_done[2][2], item_full[kItems],
     // item_empty[kItems], drain
@@ -101,17 +108,39 @@ struct Cfg {
 
 struct KParams {
     PromptArgs a;
-    float kq;  // softmax scale * log2(e)
+    float kq;           // softmax scale * log2(e)
+    uint32_t* counter;  // items taken beyond the first of each block; null: there are no more
 };
 
+// Of one sequence (n queries, m keys, groups of G heads), the number of pairs of
+// query tiles whose first tile needs at least `steps` steps of 64 keys (pairs
+// are numbered from the last tile down, so these come first).
+__device__ __forceinline__ int64_t pairs_from(int n, int m, int G, bool causal, int64_t steps) {
+    const int64_t F = static_cast<int64_t>((n + 127) / 128) * G;
+    if (steps <= 0) return (F + 1) / 2;
+    // the first tile's last row sees m - n + min(n, its end) keys (causal) or m
+    const int64_t z = (steps - 1) * 64 + 1 - m + (causal ? n : 0);
+    if (!causal) return z <= 0 ? (F + 1) / 2 : 0;
+    if (z > n) return 0;
+    const int64_t first = z <= 0 ? 0 : (z - 1) / 128 * G;  // smallest number of such a tile
+    return F - 1 < first ? 0 : (F - 1 - first) / 2 + 1;
+}
+
 // Of the 16 exponential pairs of 32 columns, this many are computed on the FMA
-// pipe instead of the MUFU.
-constexpr int kFmaPairs = 6;
+// pipe instead of the MUFU.  A pair takes the MUFU 16 cycles a warp (8 an
+// instruction), the FMA pipe 14 (seven packed instructions); measured at d = 128
+// and 64, 8,192 keys: 0 pairs 1010 and 576 TFLOP/s, 3 1071 and 615, 4 1084 and
+// 631, 5 1082 and 604, 6 1075 and 590.
+constexpr int kFmaPairs = 4;
 __host__ __device__ constexpr bool fma_pair(int q) { return (q * kFmaPairs) % 16 < kFmaPairs; }
 
-// 2^w for two values w <= 8 on the FMA pipe: exp2_fma_x2's range reduction and polynomial (max relative
-// error 2.3e-7) with the clamp at -127, where the exponent field becomes 0: what is below 2^-126 ends as a subnormal
-// below it, which the rounding of P to 16 bits and the row sum take for (nearly) nothing.
+// 2^w for two values on the FMA pipe: n = round(w) from the add of 1.5 * 2^23,
+// 2^f for f = w - n in [-1/2, 1/2] from the degree-4 polynomial of least largest
+// relative error among those with p(0) = 1 (csrc/exp2_pair_fit.py; 2.9e-6 in
+// fp32, mean 3.4e-7: a seven-hundredth of bf16's rounding of P), n added to the
+// exponent field.  Inputs are clamped at -127: there f = 0 and p = 1, so the
+// exponent field becomes 0 and the result exactly 0; between -127 and -126 it is
+// a subnormal.
 __device__ __forceinline__ void exp2_pair(float w0, float w1, float& v0, float& v1) {
     w0 = fmaxf(w0, -127.f);
     w1 = fmaxf(w1, -127.f);
@@ -122,9 +151,7 @@ __device__ __forceinline__ void exp2_pair(float w0, float w1, float& v0, float& 
         "add.rn.f32x2 t, w, c;\n\t"
         "sub.rn.f32x2 n, t, c;\n\t"
         "sub.rn.f32x2 f, w, n;\n\t"
-        "mov.b64 p, {%12, %12};\n\t"
-        "mov.b64 c, {%11, %11};\n\t"
-        "fma.rn.f32x2 p, p, f, c;\n\t"
+        "mov.b64 p, {%11, %11};\n\t"
         "mov.b64 c, {%10, %10};\n\t"
         "fma.rn.f32x2 p, p, f, c;\n\t"
         "mov.b64 c, {%9, %9};\n\t"
@@ -137,8 +164,7 @@ __device__ __forceinline__ void exp2_pair(float w0, float w1, float& v0, float& 
         "mov.b64 {%2, %3}, t;\n\t}"
         : "=r"(p0), "=r"(p1), "=r"(t0), "=r"(t1)
         : "f"(w0), "f"(w1), "f"(12582912.0f),  // 1.5 * 2^23
-          "f"(0x1.000002p+0f), "f"(0x1.62e428p-1f), "f"(0x1.ebf91ap-3f), "f"(0x1.c6b782p-5f), "f"(0x1.3d0ba4p-7f),
-          "f"(0x1.5bc922p-10f));
+          "f"(1.0f), "f"(0x1.62e12ap-1f), "f"(0x1.ec0382p-3f), "f"(0x1.c9fd1ep-5f), "f"(0x1.3a007ap-7f));
     v0 = __uint_as_float(p0 + (t0 << 23));
     v1 = __uint_as_float(p1 + (t1 << 23));
 }
@@ -385,23 +411,46 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             // ------------------------------------------------------------ scheduler
             const PromptArgs& a = p.a;
             const int G = a.Hq / a.Hkv;
-            int64_t before = 0;  // items of the sequences before the window
+            const bool causal = a.causal;
+            // The class of the longest item, and a look at all offsets.
+            int64_t longest = 0;
+            for (int b = lane; b < a.B; b += 32) {
+                int q0, q1, k0, k1;
+                bool ok = packed_range(a.q_offsets, b, a.total_q, q0, q1);
+                ok &= packed_range(a.kv_offsets, b, a.total_kv, k0, k1);
+                if (!ok && blockIdx.x == 0) atomicOr(status, kStatusInvalid);
+                if (q1 > q0) longest = max(longest, static_cast<int64_t>(k1 - k0 + 63) / 64);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+            int cls = 64 - __clzll(longest);  // items of [2^(cls - 1), 2^cls) steps; class 0: of none
+            // A window of 32 sequences in the class, a lane each.
+            int64_t before = 0;  // items before the window
             int b0 = -32, k = 0;
-            int64_t incl = 0, count = 0, total = 0;
+            int64_t incl = 0, count = 0, total = 0, larger = 0;
             int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
             bool more = true;
-            for (int64_t item = blockIdx.x; more; item += gridDim.x, ++k) {
-                while (b0 < 0 || (item >= before + total && b0 < a.B)) {  // next window of 32 sequences
+            for (int64_t item = blockIdx.x; more; ++k) {
+                while (b0 < 0 || (item >= before + total && cls >= 0)) {
                     before += total;
                     b0 += 32;
+                    if (b0 >= a.B) {
+                        b0 = 0;
+                        if (--cls < 0) {
+                            total = 0;
+                            break;
+                        }
+                    }
                     const int b = b0 + lane;
                     count = 0;
                     if (b < a.B) {
-                        bool ok = packed_range(a.q_offsets, b, a.total_q, q0, q1);
-                        ok &= packed_range(a.kv_offsets, b, a.total_kv, k0, k1);
-                        if (!ok && blockIdx.x == 0) atomicOr(status, kStatusInvalid);
-                        const int64_t tiles = (static_cast<int64_t>(q1 - q0) + 127) / 128 * G;
-                        count = (tiles + 1) / 2 * a.Hkv;
+                        packed_range(a.q_offsets, b, a.total_q, q0, q1);
+                        packed_range(a.kv_offsets, b, a.total_kv, k0, k1);
+                        if (q1 > q0) {
+                            larger = pairs_from(q1 - q0, k1 - k0, G, causal, int64_t(1) << cls);
+                            const int64_t least = cls == 0 ? 0 : int64_t(1) << (cls - 1);
+                            count = (pairs_from(q1 - q0, k1 - k0, G, causal, least) - larger) * a.Hkv;
+                        }
                     }
                     incl = count;
 #pragma unroll
@@ -421,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     it.last = more ? 0 : 1;
                     if (more) {
                         const int64_t r = at - (incl - count);
-                        const int64_t pair = r / a.Hkv;
+                        const int64_t pair = larger + r / a.Hkv;
                         const int n = q1 - q0, m = k1 - k0;
                         const int64_t F = static_cast<int64_t>((n + 127) / 128) * G;
                         it.kv_head = static_cast<int>(r % a.Hkv);
@@ -444,6 +493,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     mbar_arrive(bar_item_full + s);
                 }
                 __syncwarp();
+                if (p.counter == nullptr) {  // no more items than blocks
+                    item = INT64_MAX;
+                } else if (more) {
+                    uint32_t taken = 0;
+                    if (lane == 0) taken = atomicAdd(p.counter, 1u);
+                    item = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, taken, 0);
+                }
             }
         }
     } else {
@@ -501,14 +557,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
                 uint32_t pw[32];
 #pragma unroll
+                for (int c = 0; c < 32; ++c) ffma2_bcast(sv[2 * c], sv[2 * c + 1], sv[2 * c], sv[2 * c + 1], kq, bias);
+#pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    float w0, w1, v0, v1;
-                    ffma2_bcast(w0, w1, sv[2 * c], sv[2 * c + 1], kq, bias);
+                    float v0, v1;
                     if (fma_pair(c % 16)) {
-                        exp2_pair(w0, w1, v0, v1);
+                        exp2_pair(sv[2 * c], sv[2 * c + 1], v0, v1);
                     } else {
-                        v0 = ex2_approx(w0);
-                        v1 = ex2_approx(w1);
+                        v0 = ex2_approx(sv[2 * c]);
+                        v1 = ex2_approx(sv[2 * c + 1]);
                     }
                     fadd2(sum[2 * (c & 1)], sum[2 * (c & 1) + 1], v0, v1);
                     pw[c] = narrow2<FP16>(v0, v1);
@@ -563,25 +620,39 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 const int u = steps + n - 1;
                 if (!wait(bar_o_done + 2 * t + (u & 1), (u >> 1) & 1)) break;
                 tc_fence_after_sync();
+                // Through shared memory, 64 channels at a time, so that a store writes four whole 128-byte lines
+                // (a thread's own row at a time, it would touch 32).
+                uint8_t* stage = smem + C::kOffStage + warp * C::kStageBytes;
+                uint16_t* rows = p.a.o + (it.q_row[t] + (warp & 3) * 32) * p.a.o_token + it.q_head[t] * p.a.o_head;
+                const int rows_here = it.rows[t] - (warp & 3) * 32;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t r[32];
-                    tmem_ld32_sync(t_o + 32 * c, r);
-                    uint32_t w[16];
+                for (int c = 0; c < D / 64; ++c) {
                     float odd = 0.f;  // NaN if a value is infinite or NaN
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float v0 = __uint_as_float(r[2 * i]), v1 = __uint_as_float(r[2 * i + 1]);
-                        odd = fmaf(v0, 0.f, fmaf(v1, 0.f, odd));
-                        w[i] = m_run == -INFINITY ? 0u : narrow2<FP16>(v0 * inv, v1 * inv);
-                    }
-                    spoiled |= odd != 0.f;
-                    if (valid) {
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[32];
+                        tmem_ld32_sync(t_o + 64 * c + 32 * h, r);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float v0 = __uint_as_float(r[2 * i]), v1 = __uint_as_float(r[2 * i + 1]);
+                            odd = fmaf(v0, 0.f, fmaf(v1, 0.f, odd));
+                            w[i] = m_run == -INFINITY ? 0u : narrow2<FP16>(v0 * inv, v1 * inv);
+                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) =
+                            *reinterpret_cast<uint4*>(stage + lane * 128 + ((4 * h + i) ^ (lane & 7)) * 16) =
                                 make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                     }
+                    spoiled |= odd != 0.f;
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3), e = lane & 7;
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (e ^ (r & 7)) * 16);
+                        if (r < rows_here) *reinterpret_cast<uint4*>(rows + r * p.a.o_token + 64 * c + 8 * e) = v;
+                    }
+                    __syncwarp();
                 }
                 tc_fence_before_sync();
             } else if (valid) {
@@ -668,6 +739,11 @@ cudaError_t launch_impl(const PromptArgs& a, cudaStream_t stream) {
     const int64_t tiles = a.total_q / 128 + min(static_cast<int64_t>(a.B), a.total_q);
     const int64_t most = (tiles * G + 1) / 2 * a.Hkv + static_cast<int64_t>(a.B) * a.Hkv;
     const int grid = static_cast<int>(min(most, static_cast<int64_t>(sm_count(dev))));
+    if (most > grid) {
+        kp.counter = a.status + kCounterWord;
+        e = cudaMemsetAsync(kp.counter, 0, sizeof(uint32_t), stream);
+        if (e != cudaSuccess) return e;
+    }
     prompt_kernel<D, FP16><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, kp);
     return cudaGetLastError();
 }
