@@ -127,6 +127,7 @@ struct StoreArgs {
     int64_t k_token, k_head, v_token, v_head, table_stride, tokens;
     int B, Hkv, d, page, page_shift, max_pages, num_pages;
     int fp16;
+    int per_block;           // cells (head, K or V) of a page that a block stores; set by the launcher
 };
 cudaError_t launch_cache_store(const StoreArgs& a, cudaStream_t stream);
 
