@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(StoreCfg<D, PAGE>::kThreads, StoreCfg<D, PAGE>
         }
         before += total;
         __syncthreads();
-        if (s_item[0] >= 0 || static_cast<int>(blockIdx.x) < before) break;
+        // (the first block looks at the whole batch, for lengths to report)
+        if (s_item[0] >= 0 && (blockIdx.x > 0 || blockIdx.y > 0)) break;
     }
     if (s_item[0] < 0) return;
     const int pg = a.table[static_cast<int64_t>(s_item[0]) * a.table_stride + s_item[1]];

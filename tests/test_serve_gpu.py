@@ -339,6 +339,20 @@ def test_store_refuses_bad_pages_and_lengths():
             assert torch.equal(c[bad], w[bad])
 
 
+def test_store_reports_a_bad_length_anywhere_in_a_large_batch():
+    g, B = gen(28), 700
+    x = randn(g, B, 1, 64)
+    table = [[b] for b in range(B)]
+    for bad in (0, 255, 256, 699):
+        held = [3] * B
+        held[bad] = 16
+        cache, status = make_cache(gen(9), B, 1, 16, 64), i32([0])
+        before = cache[0].clone()
+        mx.mxattn_cache_store(x, x, *cache, i32(table), i32(range(B + 1)), i32(held), status=status)
+        assert int(status) == 1
+        assert torch.equal(cache[0][bad], before[bad]) and not torch.equal(cache[0][(bad + 1) % B], before[(bad + 1) % B])
+
+
 def check_attend(q, cache, table, lens, scale=0.0, status=0, **kw):
     ws = mx.new_cache_attend_workspace(q.shape[1], cache[0].shape[1], q.shape[2])
     o, lse = mx.mxattn_cache_attend(q, *cache, i32(table), i32(lens), scale, workspace=ws, **kw)
@@ -434,6 +448,26 @@ def test_attend_nan_queries_and_keys():
     for x in (o, want):
         x[1, 2], x[2, 3], x[3, :, 9] = 0, 0, 0
     ref.close(o, want, to)
+
+
+def test_attend_many_sequences():
+    """More sequences than threads of a block, most of them short or empty, one long among them."""
+    g = gen(29)
+    lens = [(5 * i) % 40 for i in range(900)]
+    lens[617] = 3000
+    cache, table = fill(g, lens, 1, 16, 64, BF)
+    check_attend(randn(g, 900, 4, 64), cache, table, lens)
+
+
+def test_attend_nothing_cached():
+    q = randn(gen(1), 3, 4, 64)
+    empty = [torch.zeros((0, 2, 16, 64), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    empty += [torch.zeros((0, 2), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    o, lse = mx.mxattn_cache_attend(q, *empty, torch.zeros((3, 0), dtype=torch.int32, device="cuda"), i32([0, 0, 0]))
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    ws = mx.new_cache_attend_workspace(4, 2, 64)
+    o, lse = mx.mxattn_cache_attend(q, *empty, i32([[0], [1], [2]]), i32([16, 3, 0]), workspace=ws)
+    assert (o == 0).all() and torch.isneginf(lse).all() and mx.mxattn_workspace_status(ws) == 1
 
 
 def test_attend_shared_pages_and_strides():
