@@ -429,14 +429,17 @@ typedef enum { MXATTN_BF16 = 0, MXATTN_FP16 = 1 } mxattn_dtype;
  *   strides: {Q row, Q head, K row, K head, V row, V head, O row, O head}.
  *   offsets: device int32 [B + 1], non-decreasing, within [0, total].
  *   softmax_scale <= 0 selects 1/sqrt(d).  total_q, total_kv <= 2^30.
- *   workspace: >= mxattn_prompt_workspace_size() bytes, 256-byte aligned.
+ *   workspace: >= 256 bytes, 256-byte aligned.  With at least
+ *   mxattn_prompt_workspace_size(total_kv, d) bytes, long sequences of few
+ *   queries are cut along the keys to fill the device (up to 42 MB; 0 for a d
+ *   outside the supported set); with less, or below 2,048 keys, they are not.
  * Scores, maxima and sums are fp32; e^(s - max) is rounded to `dtype` for the
  * product with V; O is rounded once.  total_q = 0 or B = 0 launches nothing.
  * Errors: MXATTN_ERR_INVALID (null, misaligned, sizes, strides, small
  * workspace), MXATTN_ERR_UNSUPPORTED (d, sizes beyond the limits),
  * MXATTN_ERR_CUDA.
  */
-size_t mxattn_prompt_workspace_size(void);
+size_t mxattn_prompt_workspace_size(int64_t total_kv, int d);
 mxattn_status mxattn_prompt(const void* Q, const void* K, const void* V, mxattn_dtype dtype, const int32_t* q_offsets,
                             const int32_t* kv_offsets, int B, int64_t total_q, int64_t total_kv, int Hq, int Hkv,
                             int d, const int64_t* strides, int causal, float softmax_scale, void* O, float* lse,

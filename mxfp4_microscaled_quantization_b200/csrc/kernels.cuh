@@ -109,7 +109,9 @@ struct PromptArgs {
     int causal;
     int fp16;
     float scale;
+    size_t workspace_bytes;  // from the status word on
 };
+size_t prompt_workspace_bytes(int64_t total_kv, int d);
 cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t stream);
 
 // Storing tokens in the 8-bit paged cache.

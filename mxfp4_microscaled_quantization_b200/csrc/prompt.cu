@@ -16,7 +16,19 @@
 // their number of steps, the longest first, and taken as blocks become free (a
 // counter in the workspace): a ragged batch of 12 sequences ends within 2 % of an
 // even share, where every grid-th item to each block left a third of the time to
-// the slowest.  Roles (384 threads):
+// the slowest.
+//
+// Where few items are long (a chunk of a prompt on a long context, one sequence
+// with few heads), the largest classes are cut along the keys into parts: if the
+// longest item has more than 5/4 of an even share of all steps, and enough more
+// to pay for it, an item of class [2^(c-1), 2^c) into 2^c / (2/3 share) parts.  A
+// part leaves its O / l and log2 of its sum in the workspace, and a second kernel
+// joins them.  Measured, whole and cut, 32 heads of 128 on 8 key heads: 512
+// queries on 30,000 keys 436 and 276 us, 16 on 4,000 84 and 54 us, four chunks of
+// up to 512 on up to 16,000 308 and 280 us; but 4,096 causal queries of 8 heads
+// 83 and 118 us (their parts' O, 42 MB, costs more than the 36 steps won).
+//
+// Roles (384 threads):
 //   warps 0-3 / 4-7  softmax of tile A / B, a thread per query row (= TMEM
 //                    lane), 64 keys a step: the row of S from TMEM, running
 //                    maximum, P back into S's own columns in 16 bits, O rescaled
@@ -64,7 +76,6 @@ namespace mxattn {
 namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
-constexpr int kCounterWord = 16;                // of the workspace: the counter of items (the status is word 0)
 
 // One item, as the scheduler publishes it.
 struct Item {
@@ -76,8 +87,28 @@ struct Item {
     int kv_row, kv_head;
     int m;          // keys of the sequence
     int last;       // 1: no more items
-    int pad[2];
+    int slot;       // of a part (m, lim0 and kv_row count from its first key); -1: a whole item
+    int keys;       // of a part
 };
+
+// What the joining kernel needs of an item that was cut: with its first part's slot.
+struct Joint {
+    int q_row[2];
+    int q_head[2];
+    int rows[2];
+    int parts;      // 0: not the first part
+    int pad;
+};
+
+constexpr int kMinPart = 16;    // steps
+constexpr int64_t kCutKeys = 2 * kMinPart * 64;
+constexpr int kMaxParts = 320;  // slots in the workspace: what would not fit is not cut
+// The workspace: status word, counter and number of parts; Joint [kMaxParts]; for each part and tile L [128] and
+// O / l [D / 4][128][4].
+constexpr int kCounterWord = 16, kPartsWord = 32;
+constexpr size_t kJointOffset = 256, kSlotOffset = kJointOffset + kMaxParts * sizeof(Joint);
+__host__ __device__ constexpr size_t slot_floats(int d) { return 2 * 128 * (static_cast<size_t>(d) + 1); }
+
 
 template <int D>
 struct Cfg {
@@ -110,6 +141,15 @@ struct KParams {
     PromptArgs a;
     float kq;           // softmax scale * log2(e)
     uint32_t* counter;  // items taken beyond the first of each block; null: there are no more
+    uint8_t* parts;     // the workspace, if items may be cut; else null
+    int blocks;         // that an even share is taken over
+};
+
+// Whether and how far the classes of a batch are cut (scheduler and joining kernel need the same of it).
+struct Cut {
+    int64_t target = 0;   // steps of a part; 0: nothing is cut
+    int lowest = 64;      // the smallest class that is cut
+    __device__ int parts(int cls) const { return cls < lowest ? 1 : static_cast<int>(((int64_t(1) << cls) + target - 1) / target); }
 };
 
 // Of one sequence (n queries, m keys, groups of G heads), the number of pairs of
@@ -240,6 +280,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tbase = *tmem_holder;
 
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -412,18 +453,62 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             const PromptArgs& a = p.a;
             const int G = a.Hq / a.Hkv;
             const bool causal = a.causal;
-            // The class of the longest item, and a look at all offsets.
-            int64_t longest = 0;
+            // The longest item and (nearly) the sum of all, and a look at all offsets.
+            int64_t longest = 0, all_steps = 0;
             for (int b = lane; b < a.B; b += 32) {
                 int q0, q1, k0, k1;
                 bool ok = packed_range(a.q_offsets, b, a.total_q, q0, q1);
                 ok &= packed_range(a.kv_offsets, b, a.total_kv, k0, k1);
                 if (!ok && blockIdx.x == 0) atomicOr(status, kStatusInvalid);
-                if (q1 > q0) longest = max(longest, static_cast<int64_t>(k1 - k0 + 63) / 64);
+                if (q1 > q0) {
+                    const int n = q1 - q0, m = k1 - k0;
+                    longest = max(longest, static_cast<int64_t>(m + 63) / 64);
+                    const int64_t first = causal ? max(0, m - n + min(n, 128)) : m;  // keys of the first tile; the last has m
+                    all_steps += (static_cast<int64_t>((n + 127) / 128) * G + 1) / 2 * a.Hkv * ((first + m) / 128 + 1);
+                }
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+            for (int o = 16; o > 0; o >>= 1) {
+                longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+                all_steps += __shfl_xor_sync(0xffffffffu, all_steps, o);
+            }
             int cls = 64 - __clzll(longest);  // items of [2^(cls - 1), 2^cls) steps; class 0: of none
+            // The items of a class in sequence b (and those of larger classes before them).
+            auto in_class = [&](int n, int m, int c, int64_t& before) -> int64_t {
+                before = pairs_from(n, m, G, causal, int64_t(1) << c);
+                return (pairs_from(n, m, G, causal, c == 0 ? 0 : int64_t(1) << (c - 1)) - before) * a.Hkv;
+            };
+            Cut cut;
+            const int64_t share = all_steps / p.blocks;
+            int64_t used = 0;  // parts in all
+            if (p.parts != nullptr && longest > share + share / 4 && longest >= 2 * kMinPart) {
+                cut.target = max(share * 2 / 3, static_cast<int64_t>(kMinPart));
+                for (int c = cls; c > 0 && (int64_t(1) << c) > cut.target; --c) {
+                    int64_t items_here = 0, larger;
+                    for (int b = lane; b < a.B; b += 32) {
+                        int q0, q1, k0, k1;
+                        packed_range(a.q_offsets, b, a.total_q, q0, q1);
+                        packed_range(a.kv_offsets, b, a.total_kv, k0, k1);
+                        if (q1 > q0) items_here += in_class(q1 - q0, k1 - k0, c, larger);
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) items_here += __shfl_xor_sync(0xffffffffu, items_here, o);
+                    if (used == 0)  // fewer and longer parts, if those of the largest class alone would not fit
+                        while (items_here > 0 && items_here * (((int64_t(1) << c) + cut.target - 1) / cut.target) > kMaxParts &&
+                               cut.target < int64_t(1) << c)
+                            cut.target *= 2;
+                    const int64_t parts = ((int64_t(1) << c) + cut.target - 1) / cut.target;
+                    if (parts < 2 || used + items_here * parts > kMaxParts) break;
+                    used += items_here * parts;
+                    cut.lowest = c;
+                }
+                // Is it worth it?  Eight parts cost about a step: their O goes out and in again in fp32.
+                if (longest - share <= 8 + used / 8) {
+                    cut.lowest = 64;
+                    used = 0;
+                }
+            }
+            if (p.parts != nullptr && blockIdx.x == 0 && lane == 0) status[kPartsWord] = static_cast<uint32_t>(used);
             // A window of 32 sequences in the class, a lane each.
             int64_t before = 0;  // items before the window
             int b0 = -32, k = 0;
@@ -447,9 +532,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         packed_range(a.q_offsets, b, a.total_q, q0, q1);
                         packed_range(a.kv_offsets, b, a.total_kv, k0, k1);
                         if (q1 > q0) {
-                            larger = pairs_from(q1 - q0, k1 - k0, G, causal, int64_t(1) << cls);
-                            const int64_t least = cls == 0 ? 0 : int64_t(1) << (cls - 1);
-                            count = (pairs_from(q1 - q0, k1 - k0, G, causal, least) - larger) * a.Hkv;
+                            count = in_class(q1 - q0, k1 - k0, cls, larger) * cut.parts(cls);
                         }
                     }
                     incl = count;
@@ -469,7 +552,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     Item it{};
                     it.last = more ? 0 : 1;
                     if (more) {
-                        const int64_t r = at - (incl - count);
+                        const int parts = cut.parts(cls);
+                        const int64_t nth = at - (incl - count), r = nth / parts;
+                        const int part = static_cast<int>(nth - r * parts);
                         const int64_t pair = larger + r / a.Hkv;
                         const int n = q1 - q0, m = k1 - k0;
                         const int64_t F = static_cast<int64_t>((n + 127) / 128) * G;
@@ -487,6 +572,27 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                             it.lim0[t] = a.causal ? tile * 128 + 1 + m - n : m;
                             const int seen = a.causal ? min(m, it.lim0[t] + it.rows[t] - 1) : m;
                             it.n[t] = seen > 0 ? (seen + 63) / 64 : 0;
+                        }
+                        it.slot = -1;
+                        it.keys = m;
+                        if (cls >= cut.lowest) {  // a part: K tiles [j0, j1), everything counted from the first
+                            it.slot = static_cast<int>(item);
+                            const int64_t tiles = (max(it.n[0], it.n[1]) + 1) / 2;
+                            const int j0 = static_cast<int>(tiles * part / parts), j1 = static_cast<int>(tiles * (part + 1) / parts);
+                            Joint joint{};
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                joint.q_row[t] = it.q_row[t];
+                                joint.q_head[t] = it.q_head[t];
+                                joint.rows[t] = it.rows[t];
+                                it.n[t] = max(0, min(it.n[t], 2 * j1) - 2 * j0);
+                                it.lim0[t] -= 128 * j0;
+                            }
+                            joint.parts = part == 0 ? parts : 0;
+                            reinterpret_cast<Joint*>(p.parts + kJointOffset)[it.slot] = joint;
+                            it.kv_row += 128 * j0;
+                            it.m -= 128 * j0;
+                            it.keys = 128 * (j1 - j0);
                         }
                     }
                     items[s] = it;
@@ -615,11 +721,33 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             const float inv = m_run == -INFINITY ? 0.f : 1.f / l_run;
             uint16_t* out = p.a.o + (it.q_row[t] + row) * p.a.o_token + it.q_head[t] * p.a.o_head;
             float* lse = p.a.lse == nullptr ? nullptr : p.a.lse + it.q_head[t] * p.a.lse_head + it.q_row[t] + row;
+            float* part = reinterpret_cast<float*>(p.parts + kSlotOffset) + (static_cast<size_t>(max(it.slot, 0)) * 2 + t) * (slot_floats(D) / 2);
             bool spoiled = false;
             if (n > 0) {
                 const int u = steps + n - 1;
                 if (!wait(bar_o_done + 2 * t + (u & 1), (u >> 1) & 1)) break;
                 tc_fence_after_sync();
+                if (it.slot >= 0) {
+                    // A part: O / l in fp32, a float4 of channels of the 128 rows side by side.
+                    float4* o4 = reinterpret_cast<float4*>(part + 128) + row;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32_sync(t_o + 32 * c, r);
+                        float odd = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                v[e] = __uint_as_float(r[4 * i + e]);
+                                odd = fmaf(v[e], 0.f, odd);
+                            }
+                            o4[(8 * c + i) * 128] = make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+                        }
+                        spoiled |= odd != 0.f;
+                    }
+                } else {
                 // Through shared memory, 64 channels at a time, so that a store writes four whole 128-byte lines
                 // (a thread's own row at a time, it would touch 32).
                 uint8_t* stage = smem + C::kOffStage + warp * C::kStageBytes;
@@ -654,14 +782,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     }
                     __syncwarp();
                 }
+                }
                 tc_fence_before_sync();
-            } else if (valid) {
+            } else if (valid && it.slot < 0) {
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(0, 0, 0, 0);
             }
             // m_run is in units of the raw score: ln sum = m scale + ln l = (m kq + log2 l) ln 2
-            if (valid && lse != nullptr)
-                *lse = m_run == -INFINITY ? -INFINITY : fmaf(m_run, kq, log2f(l_run)) * 0.693147180559945f;
+            const float L = m_run == -INFINITY ? -INFINITY : fmaf(m_run, kq, log2f(l_run));
+            if (it.slot >= 0) part[row] = L;
+            else if (valid && lse != nullptr) *lse = L * 0.693147180559945f;
             // A row whose sum over V was spoiled by a place it does not see (its own weights' sum is finite).
             uint32_t again = __ballot_sync(0xffffffffu, p.a.causal && valid && spoiled && m_run != -INFINITY &&
                                                             l_run - l_run == 0.f);
@@ -670,12 +800,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 const int who = __ffs(again) - 1;
                 again &= again - 1;
                 const int r = (warp & 3) * 32 + who;
-                const int see = min(it.m, it.lim0[t] + r);
+                const int see = min(min(it.m, it.keys), it.lim0[t] + r);
                 attend_row<D, FP16>(p.a.q + (it.q_row[t] + r) * p.a.q_token + it.q_head[t] * p.a.q_head,
                                     p.a.k + it.kv_row * p.a.k_token + it.kv_head * p.a.k_head,
                                     p.a.v + it.kv_row * p.a.v_token + it.kv_head * p.a.v_head, p.a.k_token,
                                     p.a.v_token, see, p.a.scale,
-                                    p.a.o + (it.q_row[t] + r) * p.a.o_token + it.q_head[t] * p.a.o_head, nullptr);
+                                    p.a.o + (it.q_row[t] + r) * p.a.o_token + it.q_head[t] * p.a.o_head,
+                                    it.slot >= 0 ? part + 128 + 4 * r : nullptr);
             }
             steps += n;
             slot += (max(it.n[0], it.n[1]) + 1) / 2 * 2;
@@ -686,6 +817,51 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if (warp == 9) {
         tc_fence_after_sync();
         tmem_dealloc(tbase, 512);
+    }
+}
+
+// Joins the parts of the items that were cut, in their order: o = sum_c w_c o_c /
+// sum_c w_c, w_c = 2^(L_c - max L).  Blocks go over the slots; a block takes a
+// tile of an item, a thread half of a row's channels.
+template <int D, bool FP16>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ KParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int used = min(kMaxParts, static_cast<int>(p.a.status[kPartsWord]));
+    const int row = threadIdx.x & 127, half = threadIdx.x >> 7;
+    for (int at = blockIdx.x; at < 2 * used; at += gridDim.x) {
+        const int slot = at >> 1, t = at & 1;
+        const Joint joint = reinterpret_cast<const Joint*>(p.parts + kJointOffset)[slot];
+        if (row >= joint.rows[t] || slot + joint.parts > kMaxParts) continue;
+        const float* first = reinterpret_cast<const float*>(p.parts + kSlotOffset) + (static_cast<size_t>(slot) * 2 + t) * (slot_floats(D) / 2);
+        float top = -INFINITY;
+        for (int c = 0; c < joint.parts; ++c) top = fmaxf(top, first[c * slot_floats(D) + row]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float acc[D / 2] = {}, total = 0.f;
+        for (int c = 0; c < joint.parts; ++c) {
+            const float L = first[c * slot_floats(D) + row];
+            if (L == -INFINITY) continue;  // the row sees no key of the part
+            const float w = exp2f(L - base);
+            total += w;
+            const float4* o4 = reinterpret_cast<const float4*>(first + c * slot_floats(D) + 128) + half * (D / 8) * 128 + row;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const float4 v = o4[i * 128];
+                acc[4 * i] = fmaf(w, v.x, acc[4 * i]);
+                acc[4 * i + 1] = fmaf(w, v.y, acc[4 * i + 1]);
+                acc[4 * i + 2] = fmaf(w, v.z, acc[4 * i + 2]);
+                acc[4 * i + 3] = fmaf(w, v.w, acc[4 * i + 3]);
+            }
+        }
+        if (joint.parts == 0) continue;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        uint16_t* out = p.a.o + (joint.q_row[t] + row) * p.a.o_token + joint.q_head[t] * p.a.o_head + half * (D / 2);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            *reinterpret_cast<uint4*>(out + 8 * i) =
+                make_uint4(narrow2<FP16>(acc[8 * i] * inv, acc[8 * i + 1] * inv), narrow2<FP16>(acc[8 * i + 2] * inv, acc[8 * i + 3] * inv),
+                           narrow2<FP16>(acc[8 * i + 4] * inv, acc[8 * i + 5] * inv), narrow2<FP16>(acc[8 * i + 6] * inv, acc[8 * i + 7] * inv));
+        if (half == 0 && p.a.lse != nullptr)
+            p.a.lse[joint.q_head[t] * p.a.lse_head + joint.q_row[t] + row] = (base + log2f(total)) * 0.693147180559945f;
     }
 }
 
@@ -744,8 +920,29 @@ cudaError_t launch_impl(const PromptArgs& a, cudaStream_t stream) {
         e = cudaMemsetAsync(kp.counter, 0, sizeof(uint32_t), stream);
         if (e != cudaSuccess) return e;
     }
-    prompt_kernel<D, FP16><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, kp);
-    return cudaGetLastError();
+    kp.blocks = sm_count(dev);
+    const bool may_cut = a.total_kv >= kCutKeys && a.workspace_bytes >= prompt_workspace_bytes(a.total_kv, D);
+    if (may_cut) kp.parts = reinterpret_cast<uint8_t*>(a.status);
+    // a part more for each block, where items may be cut: the grid and the counter are for them too
+    const int blocks = may_cut ? kp.blocks : grid;
+    if (may_cut && kp.counter == nullptr) {
+        kp.counter = a.status + kCounterWord;
+        e = cudaMemsetAsync(kp.counter, 0, sizeof(uint32_t), stream);
+        if (e != cudaSuccess) return e;
+    }
+    prompt_kernel<D, FP16><<<blocks, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, kp);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !may_cut) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * kp.blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prompt_join_kernel<D, FP16>, kp);
 }
 
 }  // namespace
@@ -754,6 +951,12 @@ int sm_count(int dev) {
     static int count[kMaxDevices] = {};
     if (count[dev] == 0) cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev);
     return count[dev] > 0 ? count[dev] : 1;
+}
+
+// Below kCutKeys keys in all, no item has the steps for two parts.
+size_t prompt_workspace_bytes(int64_t total_kv, int d) {
+    if (total_kv < kCutKeys) return 256;
+    return (kSlotOffset + kMaxParts * slot_floats(d) * sizeof(float) + 255) / 256 * 256;
 }
 
 cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t stream) {

@@ -88,10 +88,11 @@ __device__ __forceinline__ float warp_sum(float x) {
 // One attention row, o = softmax(q K^T scale) V over keys 0 .. n - 1, by one
 // warp in fp32: a lane per key for the scores, a lane per D / 32 channels for
 // the sum over V.  No key behind n is read, so nothing that a row may not see
-// reaches it.  k and v: row 0 of the sequence, strides in elements.
+// reaches it.  k and v: row 0 of the keys, strides in elements.  Writes o, or
+// with `part` instead channel c, in fp32, to part[(c / 4) * 512 + c % 4].
 template <int D, bool FP16>
 __device__ __noinline__ void attend_row(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t k_stride,
-                                        int64_t v_stride, int n, float scale, uint16_t* o, float* lse) {
+                                        int64_t v_stride, int n, float scale, uint16_t* o, float* part) {
     constexpr int C = D / 32;  // channels of a lane
     const int lane = threadIdx.x & 31;
     float m = -INFINITY, l = 0.f, acc[C];
@@ -138,10 +139,14 @@ __device__ __noinline__ void attend_row(const uint16_t* q, const uint16_t* k, co
         m = m_new;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: zeros, lse -inf
+    if (part != nullptr) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) part[(lane * C + c) / 4 * 512 + (lane * C + c) % 4] = acc[c] * inv;
+        return;
+    }
 #pragma unroll
     for (int c = 0; c < C; c += 2)
         *reinterpret_cast<uint32_t*>(o + lane * C + c) = narrow2<FP16>(acc[c] * inv, acc[c + 1] * inv);
-    if (lse != nullptr && lane == 0) *lse = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 }  // namespace mxattn

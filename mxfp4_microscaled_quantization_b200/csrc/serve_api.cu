@@ -42,7 +42,10 @@ int page_shift(int page) {
 
 }  // namespace
 
-MXATTN_API size_t mxattn_prompt_workspace_size(void) { return kStatusBytes; }
+MXATTN_API size_t mxattn_prompt_workspace_size(int64_t total_kv, int d) {
+    if (total_kv < 0 || (d != 64 && d != 128)) return 0;
+    return mxattn::prompt_workspace_bytes(total_kv, d);
+}
 
 MXATTN_API mxattn_status mxattn_prompt(const void* Q, const void* K, const void* V, mxattn_dtype dtype,
                                        const int32_t* q_offsets, const int32_t* kv_offsets, int B, int64_t total_q,
@@ -74,6 +77,7 @@ MXATTN_API mxattn_status mxattn_prompt(const void* Q, const void* K, const void*
     a.q_offsets = q_offsets;
     a.kv_offsets = kv_offsets;
     a.status = static_cast<uint32_t*>(workspace);
+    a.workspace_bytes = workspace_bytes;
     a.q_token = s[0], a.q_head = s[1], a.k_token = s[2], a.k_head = s[3];
     a.v_token = s[4], a.v_head = s[5], a.o_token = s[6], a.o_head = s[7];
     a.lse_head = lse_stride;

@@ -90,7 +90,7 @@ def lib() -> ctypes.CDLL:
         L.mxattn_nvfp4_prepare.restype = i32
         L.mxattn_nvfp4_attend.argtypes = [i32, i32, i32, i32, i32, i32, f32, P, P, u64, P]
         L.mxattn_nvfp4_attend.restype = i32
-        L.mxattn_prompt_workspace_size.argtypes = []
+        L.mxattn_prompt_workspace_size.argtypes = [i64, i32]
         L.mxattn_prompt_workspace_size.restype = u64
         L.mxattn_prompt.argtypes = [P, P, P, i32, P, P, i32, i64, i64, i32, i32, i32, P, i32, f32, P, P, i64, P, u64, P]
         L.mxattn_prompt.restype = i32
@@ -579,9 +579,15 @@ def _serve(fn, where, like, stream, *args):
         raise MxattnError(status, where)
 
 
-def new_prompt_workspace(device="cuda") -> torch.Tensor:
-    """Workspace of mxattn_prompt, its status word cleared."""
-    return torch.zeros(int(lib().mxattn_prompt_workspace_size()), dtype=torch.uint8, device=device)
+def new_prompt_workspace(total_kv: int = 0, d: int = 128, device="cuda") -> torch.Tensor:
+    """Workspace of mxattn_prompt for up to total_kv keys of d channels, its status word cleared.  (One for fewer keys
+    serves too: long sequences of few queries are then not cut along the keys.)"""
+    n = int(lib().mxattn_prompt_workspace_size(total_kv, d))
+    if n == 0:
+        raise MxattnError(2, "mxattn_prompt_workspace_size")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
 
 
 def new_cache_attend_workspace(Hq: int, Hkv: int, d: int, device="cuda") -> torch.Tensor:
@@ -607,7 +613,8 @@ def mxattn_prompt(q, k, v, q_offsets, kv_offsets=None, causal=True, softmax_scal
     if lse is None:
         lse = torch.full((Hq, Tq), float("-inf"), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(256, dtype=torch.uint8, device=q.device)
+        need = 256 if Tk < 2048 else max(256, lib().mxattn_prompt_workspace_size(Tk, d))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     strides = _strides(_I64x8, ((Hq, d), (Hkv, d), (Hkv, d), (Hq, d)),
                        (_rows("q", q, Tq, Hq, d, q), _rows("k", k, Tk, Hkv, d, q), _rows("v", v, Tk, Hkv, d, q),
                         _rows("out", out, Tq, Hq, d, q)))

@@ -31,7 +31,9 @@ def test_prompt_refusals(L):
         return L.mxattn_prompt(a["q"], a["k"], a["v"], a["dt"], a["qo"], a["ko"], a["B"], a["tq"], a["tk"], a["Hq"],
                                a["Hkv"], a["d"], _strides(a["st"]), a["causal"], F(0), a["o"], a["lse"], a["ls"], a["ws"],
                                a["wb"], None)
-    assert L.mxattn_prompt_workspace_size() == 256
+    assert L.mxattn_prompt_workspace_size(2047, 128) == 256 and L.mxattn_prompt_workspace_size(0, 64) == 256
+    assert 256 < L.mxattn_prompt_workspace_size(2048, 64) < L.mxattn_prompt_workspace_size(1 << 30, 128) < 1 << 26
+    assert L.mxattn_prompt_workspace_size(100, 96) == 0 and L.mxattn_prompt_workspace_size(-1, 64) == 0
     for kw in (dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(qo=None), dict(ko=None), dict(ws=None),
                dict(dt=2), dict(dt=-1), dict(B=-1), dict(Hq=7), dict(Hq=0), dict(Hkv=0), dict(tq=-1), dict(tk=-1),
                dict(causal=2), dict(wb=255), dict(ws=FAKE + 16), dict(q=FAKE + 8), dict(k=FAKE + 8), dict(v=FAKE + 2),

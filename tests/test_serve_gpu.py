@@ -40,8 +40,8 @@ def offsets(lens):
 
 # ------------------------------------------------------------------ prompts
 
-def check_prompt(q, k, v, qo, ko, causal, scale=0.0, **kw):
-    ws = mx.new_prompt_workspace()
+def check_prompt(q, k, v, qo, ko, causal, scale=0.0, cut=True, **kw):
+    ws = mx.new_prompt_workspace(k.shape[0] if cut else 0, q.shape[2])
     o, lse = mx.mxattn_prompt(q, k, v, i32(qo), i32(ko), causal, scale, workspace=ws, **kw)
     assert mx.mxattn_workspace_status(ws) == 0
     want, wl, to, tl = ref.prompt(q, k, v, qo, ko, causal, scale or None)
@@ -77,6 +77,54 @@ def test_prompt_long(n, Hq, Hkv, d, dtype):
     g = gen(n)
     q, k, v = randn(g, n, Hq, d, dtype=dtype, scale=2.0), randn(g, n, Hkv, d, dtype=dtype), randn(g, n, Hkv, d, dtype=dtype)
     check_prompt(q, k, v, [0, n], [0, n], True)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv,d,dtype", [
+    ([1], [5000], 2, 1, 128, BF),               # one query: every part of one item
+    ([200], [4003], 3, 1, 64, FP),              # an odd number of tiles: the last item has one
+    ([17, 64, 3], [2048, 4096, 1000], 8, 2, 128, BF),
+    ([300, 2, 40, 0], [9000, 300, 2300, 500], 4, 2, 64, BF),
+    ([3000], [2900], 1, 1, 128, FP),            # rows that see no key; parts that only later rows see
+    ([129] * 3, [3333] * 3, 5, 1, 128, BF)])
+def test_prompt_cut_along_the_keys(q_lens, kv_lens, Hq, Hkv, d, dtype, causal):
+    """Few queries on long keys: items cut into parts and joined; the same within rounding as without (a workspace too
+    small for parts)."""
+    g, qo, ko = gen(40), offsets(q_lens), offsets(kv_lens)
+    q = randn(g, qo[-1], Hq, d, dtype=dtype, scale=1.5)
+    k, v = randn(g, ko[-1], Hkv, d, dtype=dtype), randn(g, ko[-1], Hkv, d, dtype=dtype)
+    check_prompt(q, k, v, qo, ko, causal)
+    check_prompt(q, k, v, qo, ko, causal, cut=False)
+
+
+def test_prompt_cut_with_masked_junk_and_graph():
+    """NaN in keys and values that only later rows see, in the last part; then captured, replayed with other lengths."""
+    g = gen(41)
+    q, k, v = randn(g, 64, 4, 128), randn(g, 4000, 2, 128), randn(g, 4000, 2, 128)
+    k[3990], v[3990] = math.nan, math.inf
+    o, lse = mx.mxattn_prompt(q, k, v, i32([0, 64]), i32([0, 4000]))
+    clean_k, clean_v = k.clone(), v.clone()
+    clean_k[3990], clean_v[3990] = 0, 0
+    want, wl, to, tl = ref.prompt(q, clean_k, clean_v, [0, 64], [0, 4000], True)
+    seen = 64 - 10  # row 54 is the first that sees key 3990
+    ref.close(o[:seen], want[:seen], to[:seen])
+    ref.close(lse[:, :seen], wl[:, :seen], tl[:, :seen])
+    assert torch.isnan(lse[:, seen:]).all() and not torch.isfinite(o[seen:]).any()
+    ws, out, ko = mx.new_prompt_workspace(4000, 128), torch.zeros_like(q), i32([0, 4000])
+    qo, lse = i32([0, 64]), torch.zeros((4, 64), device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mx.mxattn_prompt(q, clean_k, clean_v, qo, ko, out=out, lse=lse, workspace=ws)
+    for n, m in ((64, 4000), (64, 300), (1, 4000), (40, 2500), (64, 4000)):
+        qo.copy_(i32([0, n]))
+        ko.copy_(i32([0, m]))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, wl, to, tl = ref.prompt(q[:n], clean_k, clean_v, [0, n], [0, m], True)
+        ref.close(out[:n], want, to)
+        ref.close(lse[:, :n], wl, tl)
+    assert mx.mxattn_workspace_status(ws) == 0
 
 
 def test_prompt_growing_scores():
