@@ -43,6 +43,15 @@
 //              for a product it could have had.
 //   warp 6     Q: loads the next piece's queries while the current one runs.
 // Every mbarrier wait is bounded, as in attention.cu.
+//
+// Measured: 64 sequences of 1 to 8,152 tokens (238,240), 32 heads on 8 of 128,
+// pages of 64: 85 us, 5.75 TB/s (0.88 of a copy's rate); 231,074 tokens in two
+// sequences, 64 heads on 8: 82 us, 5.75 TB/s; one sequence of 1,000 tokens 10 us.
+// Steps to that: maxima by a barrier that only asks whether one has grown, in
+// place of an exact maximum a tile (16 heads: 73 to 39 us on 61,440 tokens); page
+// exponents through the producer, in place of two dependent loads a tile (105 us
+// to 116 on the first case); ends of pieces a lane a head, in place of a loop of
+// quotients and logarithms (3.4 to 1.5 us an end).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>

@@ -129,14 +129,15 @@ def cached(val, exps, pages, n):
 
 
 def attend(q, k_codes, v_codes, k_exps, v_exps, table, lens, scale=None):
-    """-> out, lse, tolerances.  P: two (bf16) or three (fp16) E4M3 parts of p 2^(ev - EV) 2^8, EV the largest exponent
-    among the sequence's pages, so beside its relative error (2^-8, 2^-12) a value has half a subnormal step, 2^-10, of
-    2^8: 2^-18 of a weight of 1 at the scale 2^EV.  Q: as many parts of q scaled so that the largest lies in [224, 448):
-    bf16's 8 and fp16's 11 significant bits fit; smaller elements have 2^-10 of 224: 2^-17 of the row's largest."""
+    """-> out, lse, tolerances.  P' = p 2^(ev - EV) 32 (p relative to a base no more than 2^3 below the maximum, EV the
+    largest exponent so far) as three E4M3 parts, each rest scaled by 16: relative error 2^-4 a part, 2^-12 in all, and
+    half of E4M3's subnormal step, 2^-10, of the third part's unit, 2^-8 / 32: 2^-23 of a weight of 1 at the scale 2^EV.
+    Q: two (bf16) or three (fp16) parts of q scaled so that the largest element lies in (224, 448]: 8 and 11 significant
+    bits fit; smaller elements have 2^-10 of 224: 2^-17 of the row's largest."""
     B, Hq, d = q.shape
     Hkv, page = k_codes.shape[1], k_codes.shape[2]
     G, u = Hq // Hkv, U[q.dtype]
-    u_p = 2.0 ** -8 if q.dtype == torch.bfloat16 else 2.0 ** -12
+    u_p = 2.0 ** -12
     scale = scale or 1.0 / math.sqrt(d)
     out = torch.zeros((B, Hq, d), dtype=torch.float64, device=q.device)
     lse = torch.full((B, Hq), -math.inf, dtype=torch.float64, device=q.device)
@@ -158,7 +159,7 @@ def attend(q, k_codes, v_codes, k_exps, v_exps, table, lens, scale=None):
             S = float((qh.abs() @ k[g].abs().T).max()) * scale
             es = (2 * d + 16) * 2.0 ** -23 * S + 2.0 ** -17 * float(qh.abs().max()) * float(k[g].abs().sum(1).max()) * scale
             top = float(torch.exp(s.max() - l[0]))  # the weight that p = 1 stands for
-            lost = 2.0 ** -18 * top * (up[g][:, None] * v[g].abs()).sum(0)
+            lost = 2.0 ** -23 * top * (up[g][:, None] * v[g].abs()).sum(0)
             out[b, h], lse[b, h] = o[0], l[0]
             tol_o[b, h] = u * o[0].abs() + (u_p + 2 * es + (n + 64) * 2.0 ** -23) * A[0] + lost
             tol_l[b, h] = es + (n + 64) * 2.0 ** -23 + 2.0 ** -22 * l[0].abs()
