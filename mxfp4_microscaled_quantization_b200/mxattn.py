@@ -6,6 +6,7 @@ All compute happens in the library's CUDA kernels; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -561,6 +562,16 @@ def _workspace(t, like):
     return t.data_ptr()
 
 
+def _on(stream, like):
+    """Context in which to make the tensors that a call on `stream` uses: allocated, filled and given back in that
+    stream's order (nothing to do for the current stream)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    return torch.cuda.stream(stream)
+
+
 def _serve(fn, where, like, stream, *args):
     """Call `fn` with `like`'s device current, on `stream` or that device's current stream."""
     index = like.get_device()
@@ -608,13 +619,15 @@ def mxattn_prompt(q, k, v, q_offsets, kv_offsets=None, causal=True, softmax_scal
     dt = _serve_head("q", q)
     Tq, Hq, d = q.shape
     Tk, Hkv = k.shape[0], k.shape[1]
-    if out is None:
-        out = torch.zeros((Tq, Hq, d), dtype=q.dtype, device=q.device)
-    if lse is None:
-        lse = torch.full((Hq, Tq), float("-inf"), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        need = 256 if Tk < 2048 else max(256, lib().mxattn_prompt_workspace_size(Tk, d))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if out is None or lse is None or workspace is None:
+        with _on(stream, q):
+            if out is None:
+                out = torch.zeros((Tq, Hq, d), dtype=q.dtype, device=q.device)
+            if lse is None:
+                lse = torch.full((Hq, Tq), float("-inf"), dtype=torch.float32, device=q.device)
+            if workspace is None:
+                need = 256 if Tk < 2048 else max(256, lib().mxattn_prompt_workspace_size(Tk, d))
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     strides = _strides(_I64x8, ((Hq, d), (Hkv, d), (Hkv, d), (Hq, d)),
                        (_rows("q", q, Tq, Hq, d, q), _rows("k", k, Tk, Hkv, d, q), _rows("v", v, Tk, Hkv, d, q),
                         _rows("out", out, Tq, Hq, d, q)))
@@ -673,15 +686,17 @@ def mxattn_cache_attend(q, k_codes, v_codes, k_scales, v_scales, block_table, le
     ptrs, pages, Hkv, page, dc, table = _cache(k_codes, v_codes, k_scales, v_scales, block_table, q, B)
     if dc != d:
         raise ValueError(f"q has {d} channels, the cache {dc}")
-    if out is None:
-        out = torch.empty((B, Hq, d), dtype=q.dtype, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        need = _attend_workspace.get((Hq, Hkv, d))
-        if need is None:
-            need = _attend_workspace[Hq, Hkv, d] = int(lib().mxattn_cache_attend_workspace_size(Hq, Hkv, d))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if out is None or lse is None or workspace is None:
+        with _on(stream, q):
+            if out is None:
+                out = torch.empty((B, Hq, d), dtype=q.dtype, device=q.device)
+            if lse is None:
+                lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+            if workspace is None:
+                need = _attend_workspace.get((Hq, Hkv, d))
+                if need is None:
+                    need = _attend_workspace[Hq, Hkv, d] = int(lib().mxattn_cache_attend_workspace_size(Hq, Hkv, d))
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     strides = _strides(_I64x4, ((Hq, d), (Hq, d)), (_rows("q", q, B, Hq, d, q), _rows("out", out, B, Hq, d, q)))
     _serve(lib().mxattn_cache_attend, "mxattn_cache_attend", q, stream, q.data_ptr(), dt, B, Hq, Hkv, d, strides, *ptrs,
            pages, page, *table, _dense("lens", lens, torch.int32, q, (B,)), softmax_scale, out.data_ptr(),

@@ -598,6 +598,26 @@ def test_offsets_beyond_32_bits():
     check_attend(q, small, [[0, 1, 2, 3]], [400])
 
 
+def test_tensors_made_by_a_call_on_another_stream():
+    """Outputs and workspace that a call makes belong to the stream it is given: work queued on the current stream neither
+    delays nor overwrites them."""
+    g = gen(31)
+    cache, table = fill(g, [700, 30], 2, 64, 128, BF)
+    q, k, v = randn(g, 200, 8, 128), randn(g, 3000, 2, 128), randn(g, 3000, 2, 128)
+    t, n, qo, ko = i32(table), i32([700, 30]), i32([0, 150, 200]), i32([0, 2500, 3000])
+    want = [*mx.mxattn_prompt(q, k, v, qo, ko), *mx.mxattn_cache_attend(q[:2], *cache, t, n)]
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s on the current stream
+        got = [*mx.mxattn_prompt(q, k, v, qo, ko, stream=stream)]
+        got += mx.mxattn_cache_attend(q[:2], *cache, t, n, stream=stream)
+        junk = [torch.full_like(x, 5) for x in got for _ in range(3)]  # takes freed memory, on the current stream
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+        del junk
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("d,page,dtype", [(128, 64, BF), (64, 16, FP)])
