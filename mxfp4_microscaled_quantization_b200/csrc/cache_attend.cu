@@ -368,7 +368,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     if (tid == 0) {
         mbar_init(bar_q_full, 1);
-        mbar_init(bar_q_empty, 2);  // the products that read Q; the softmax, which has left the piece before
+        // The products that read Q; each softmax warp, which has left the piece before and has seen this one's Q (were
+        // a warp still to look for it, the next piece's Q would flip the parity back and it would wait for good).
+        mbar_init(bar_q_empty, 1 + 4);
         for (int s = 0; s < S; ++s) {
             mbar_init(bar_kv_full + s, 2);  // the tile's bytes, its pages' exponents (K's slot; nothing more for V's)
             mbar_init(bar_kv_empty + s, 1);
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int head0 = head * p.G + chunk * p.per, heads = min(p.per, p.G - chunk * p.per);
             const int last = it.tile0 + it.n;
             wait(bar_q_full, k & 1);
-            if (tid == 0) mbar_arrive(bar_q_empty);
+            if (lane == 0) mbar_arrive(bar_q_empty);
             const float4* col = reinterpret_cast<const float4*>(sCol + (k & 1) * NC);
             const float4* base4 = reinterpret_cast<const float4*>(sBase);
             float l[GC];

@@ -507,6 +507,20 @@ def test_attend_many_sequences():
     check_attend(randn(g, 900, 4, 64), cache, table, lens)
 
 
+@pytest.mark.parametrize("Hkv,d,page,dtype", [(24, 64, 16, FP), (8, 128, 64, BF)])
+def test_attend_blocks_of_many_one_tile_pieces(Hkv, d, page, dtype):
+    """Queries, products and weights change hands at every tile, over and over: no wait may miss its phase."""
+    g, lens = gen(31), [1 + 3 * (i % 5) for i in range(128)]
+    cache, table = fill(g, lens, Hkv, page, d, dtype)
+    q = randn(g, 128, Hkv, d, dtype=dtype)
+    o, lse = check_attend(q, cache, table, lens)
+    ws = mx.new_cache_attend_workspace(Hkv, Hkv, d)
+    for _ in range(200):
+        o2, lse2 = mx.mxattn_cache_attend(q, *cache, i32(table), i32(lens), workspace=ws)
+    assert mx.mxattn_workspace_status(ws) == 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_attend_nothing_cached():
     q = randn(gen(1), 3, 4, 64)
     empty = [torch.zeros((0, 2, 16, 64), dtype=torch.uint8, device="cuda") for _ in range(2)]
