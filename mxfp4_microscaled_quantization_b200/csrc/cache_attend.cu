@@ -16,7 +16,9 @@
 //     (224, 448]:  q = q1 + q2 (+ q3), every part the rounded rest of those
 //     before.  A part takes 4 bits, so two hold bf16's 8 significant bits and
 //     three fp16's 11, down to 2^-10 (2^-18 of the largest element).  The
-//     parts' products add up in one accumulator.
+//     parts are further rows of Q, columns of S^T that each thread adds up: a
+//     product's time is that of reading the tile's 128 rows, up to 48 columns
+//     cost no more than 16 (M 128, N 16 or 32: 40 cycles each).
 //   * P as p1 + p2 / 16 + p3 / 256, the rest scaled by 16 before it is rounded,
 //     so it does not run out of exponent:  relative error 2^-12, or 2^-23 of a
 //     weight of 1 where that is more (a long context under one strong token has
@@ -32,26 +34,31 @@
 // workspace, and a second kernel (started early by programmatic launch) joins
 // the parts in the order of the list, so results do not depend on timing.
 //
-// Roles (224 threads):
+// Roles (256 threads):
 //   warps 0-3  softmax, a thread per token of the tile (= TMEM lane of S^T), all
 //              heads of the group: maxima over the tile (redux, then shared
 //              memory), P's parts to shared memory; O^T rescaled only when a
 //              maximum has grown by more than 2^3 (P stays below 448) or a
 //              larger V exponent came; the end of each piece.
-//   warp 4     TMA producer, a lane per page, one ring for K and V tiles.
-//   warp 5     MMA issuer: S(n + 1) before PV(n), so the softmax never waits
-//              for a product it could have had.
+//   warps 4, 7 TMA producers of K and of V, a lane per page, one ring for both.
+//   warp 5     MMA issuer, one thread: S(n + 1) before PV(n), so the softmax
+//              never waits for a product it could have had.
 //   warp 6     Q: loads the next piece's queries while the current one runs.
 // Every mbarrier wait is bounded, as in attention.cu.
 //
 // Measured: 64 sequences of 1 to 8,152 tokens (238,240), 32 heads on 8 of 128,
-// pages of 64: 85 us, 5.75 TB/s (0.88 of a copy's rate); 231,074 tokens in two
-// sequences, 64 heads on 8: 82 us, 5.75 TB/s; one sequence of 1,000 tokens 10 us.
+// pages of 64: 84 us, 5.8 TB/s (0.89 of a copy's rate); 231,074 tokens in two
+// sequences, 64 heads on 8: 80 us, 5.9 TB/s; 64 of 4,000, 24 heads of 64, pages
+// of 16: 152 us, 5.2 TB/s; one sequence of 1,000 tokens 10 us.
 // Steps to that: maxima by a barrier that only asks whether one has grown, in
 // place of an exact maximum a tile (16 heads: 73 to 39 us on 61,440 tokens); page
 // exponents through the producer, in place of two dependent loads a tile (105 us
 // to 116 on the first case); ends of pieces a lane a head, in place of a loop of
-// quotients and logarithms (3.4 to 1.5 us an end).
+// quotients and logarithms (3.4 to 1.5 us an end); a second producer warp (pages
+// of 16, 64 channels: 203 to 152 us; as one code for both, for two copies of it
+// cost more cold instructions than they saved); Q's parts as columns of one
+// product, one thread that issues, no waits that another wait implies, two
+// buffers for P (K's arrival to the softmax: 950 cycles to 280).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -67,7 +74,7 @@ namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr int kTile = 128;                      // tokens
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr int kCtasPerSm = 2;
 constexpr int kPairCost = 1;                    // a pair's start and end, in tiles
 constexpr int kMaxCols = 16;                    // query heads a block handles together
@@ -78,22 +85,25 @@ constexpr float kPUnit = 32.f;                  // P's unit: 32 * 2^3 <= 448
 // D channels, GC query heads (1 .. GC used), PARTS E4M3 parts of Q.
 template <int D, int GC, int PARTS>
 struct Cfg {
-    static constexpr int NC = 16;                    // columns of S^T
-    static constexpr int NO = NC * kPParts;          // columns of O^T
+    static constexpr int NC = kMaxCols;
+    // Columns of S^T and O^T: column part * GC + g is a part of head g, up to the next multiple of 16.
+    static constexpr int NS = (PARTS * GC + 15) / 16 * 16;
+    static constexpr int NO = (kPParts * GC + 15) / 16 * 16;
     static constexpr int kTileBytes = kTile * D;     // a K or V tile
-    static constexpr int kQBytes = NC * D;           // one part of Q
+    static constexpr int kQBytes = NS * D;
     static constexpr int kPBytes = kTile * NO;       // P of a tile, [column chunk of 16][token][16]
-    static constexpr int kFixed = PARTS * kQBytes + kPBytes + 2048;
+    static constexpr int kPBuffers = GC < 16 ? 2 : 1;  // with 16 heads a second one would cost a place of the ring
+    static constexpr int kFixed = kQBytes + kPBuffers * kPBytes + 2048;
     // 228 KB an SM, 1 KB of each block is the system's
-    static constexpr int kSlots = ((228 * 1024) / kCtasPerSm - 1024 - 1024 - kFixed) / kTileBytes;
+    static constexpr int kSlots = ((228 * 1024) / kCtasPerSm - 1024 - 1024 - kFixed) / kTileBytes / 2 * 2;  // K, V in turn
     static_assert(kSlots >= 4, "ring");
     static constexpr int kOffQ = 0;
-    static constexpr int kOffRing = (kOffQ + PARTS * kQBytes + 1023) / 1024 * 1024;
+    static constexpr int kOffRing = (kOffQ + kQBytes + 1023) / 1024 * 1024;
     static constexpr int kOffP = kOffRing + kSlots * kTileBytes;
-    static constexpr int kOffMax = kOffP + kPBytes;               // float [NC][4], then u32 [4]
+    static constexpr int kOffMax = kOffP + kPBuffers * kPBytes;               // float [NC][4], then u32 [4]
     static constexpr int kOffBar = kOffMax + NC * 16 + 16;
-    // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], s_empty[2], p_full, pv_done, drain
-    static constexpr int kNumBars = 2 + 2 * kSlots + 4 + 2 + 1;
+    // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], p_full[2], pv_done[2], drain
+    static constexpr int kNumBars = 2 + 2 * kSlots + 6 + 1;
     static constexpr int kOffCol = (kOffBar + kNumBars * 8 + 15) / 16 * 16;  // float [2][NC]: 2^eq * scale * log2 e
     static constexpr int kOffBase = kOffCol + 2 * NC * 4;         // float [NC]: the maxima that P is relative to
     // uint2 [kRing][8]: the exponents of a tile's pages, as long as its K or V tile may be in the ring
@@ -102,9 +112,9 @@ struct Cfg {
     static constexpr int kOffMisc = kOffScale + kScaleRing * 64;  // TMEM base, abort flag
     static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
     static_assert(kSmemBytes <= 113 * 1024, "two blocks an SM");
-    // TMEM: S [2][NC], O [NO]
-    static constexpr uint32_t kCols = 128;
-    static_assert(2 * NC + NO <= kCols, "TMEM");
+    // TMEM: S [2][NS], O [NO]
+    static constexpr uint32_t kCols = 2 * NS + NO <= 64 ? 64 : 2 * NS + NO <= 128 ? 128 : 256;
+    static_assert(2 * NS + NO <= kCols, "TMEM");
     static_assert(kCtasPerSm * kCols <= 512, "TMEM");
     static constexpr uint32_t kLayout = D == 128 ? kLayoutSw128 : kLayoutSw64;
     static constexpr uint32_t kSbo = 8 * D;          // 8 rows of K, V or Q
@@ -137,31 +147,22 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// N consecutive fp32 columns of this thread's TMEM lane (N = 4, 8 or 16).
+// N (a multiple of 16) consecutive fp32 columns of this thread's TMEM lane.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* v) {
-#define MXATTN_R4(b) "=r"(v[b]), "=r"(v[b + 1]), "=r"(v[b + 2]), "=r"(v[b + 3])
-    if constexpr (N == 4) {
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
-                     : MXATTN_R4(0)
-                     : "r"(taddr)
-                     : "memory");
-    } else if constexpr (N == 8) {
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-            "tcgen05.wait::ld.sync.aligned;"
-            : MXATTN_R4(0), MXATTN_R4(4)
-            : "r"(taddr)
-            : "memory");
-    } else {
-        static_assert(N == 16, "columns");
+#define MXATTN_R4(op, b) op(v[b]), op(v[b + 1]), op(v[b + 2]), op(v[b + 3])
+#pragma unroll
+    for (int c = 0; c < N; c += 16)
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-            "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-            : MXATTN_R4(0), MXATTN_R4(4), MXATTN_R4(8), MXATTN_R4(12)
-            : "r"(taddr)
+            "%15}, [%16];"
+            : MXATTN_R4("=r", c), MXATTN_R4("=r", c + 4), MXATTN_R4("=r", c + 8), MXATTN_R4("=r", c + 12)
+            : "r"(taddr + c)
             : "memory");
-    }
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // nothing that uses the columns may move up past the wait
+#pragma unroll
+    for (int c = 0; c < N; c += 4) asm volatile("" : MXATTN_R4("+r", c)::"memory");
 #undef MXATTN_R4
 }
 
@@ -328,6 +329,11 @@ __device__ __forceinline__ int page_at(const AttendArgs& a, int b, int index) {
     return a.table[static_cast<int64_t>(b) * a.table_stride + index];
 }
 
+// A wait that does not end at once.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status) {
+    return mbar_wait_bounded(bar, parity, abort_flag, status, kStatusTimeout, kTimeoutNs);
+}
+
 template <int D, bool FP16, int GC>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     cache_attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -351,10 +357,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint64_t* bar_kv_full = bars + 2;
     uint64_t* bar_kv_empty = bar_kv_full + S;
     uint64_t* bar_s_full = bar_kv_empty + S;
-    uint64_t* bar_s_empty = bar_s_full + 2;
-    uint64_t* bar_p_full = bar_s_empty + 2;
-    uint64_t* bar_pv_done = bar_p_full + 1;
-    uint64_t* bar_drain = bar_pv_done + 1;
+    uint64_t* bar_p_full = bar_s_full + 2;
+    uint64_t* bar_pv_done = bar_p_full + 2;
+    uint64_t* bar_drain = bar_pv_done + 2;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     const AttendArgs& a = p.a;
@@ -377,16 +382,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar_s_full + s, 1);
-            mbar_init(bar_s_empty + s, 128);
+            mbar_init(bar_p_full + s, 128);  // P(n + 1) may be there before P(n) has been looked for: S(n + 1) comes first
+            mbar_init(bar_pv_done + s, 1);
         }
-        mbar_init(bar_p_full, 128);
-        mbar_init(bar_pv_done, 1);
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
         fence_mbarrier_init();
     }
     // Q's rows behind the group's heads stay zero.
-    for (int i = tid; i < PARTS * C::kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < C::kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (warp == 5) {
         tmem_alloc(tmem_holder, C::kCols);
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     tc_fence_after_sync();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tbase = *tmem_holder;
-    const uint32_t col_o = 2 * NC;
+    const uint32_t col_o = 2 * C::NS;
 
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu,
@@ -419,20 +423,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     };
     Pieces it(a, pairs, x0, x1, at.base, at.b);
 
-    if (warp == 4) {
-        // ---------------------------------------------------------------- TMA producer, a lane per page of the tile
+    if (warp == 4 || warp == 7) {
+        // ---------------------------------------------------------------- TMA producers, a lane per page of the tile
+        // Warp 4 brings K tiles and their pages' exponents, warp 7 V tiles: two warps, because issuing the copies of
+        // small pages is what takes their time (1 KB each, 64 channels: 203 us with one warp, 162 with two).
+        const int kv = warp == 4 ? 0 : 1;
+        const CUtensorMap* tm = kv ? &tmV : &tmK;
         const int ppt = kTile >> P;  // pages of a tile
-        int slot = 0;
+        int n = 0;                   // running number of the tile, in running place 2 n + kv
+        int at = kv;                 // that place in the ring, and its phase
+        uint32_t phase = 0;
         bool ok = true;
         // The exponents of a tile's pages follow one tile behind its copies, so their loads have time to arrive.
         uint32_t late_ks = 0, late_vs = 0;
         bool late_good = false;
-        auto publish = [&](int k_slot) {  // of the tile whose K is in running slot k_slot
+        int late_at = 0;
+        auto publish = [&](int m) {
             if (lane < ppt)
-                sScale[k_slot / 2 % C::kScaleRing * 8 + lane] =
+                sScale[m % C::kScaleRing * 8 + lane] =
                     make_uint2(__float_as_uint(log2_to_float(late_ks)), late_vs | (late_good ? 0x100u : 0u));
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_kv_full + k_slot % S);
+            if (lane == 0) mbar_arrive(bar_kv_full + late_at);
             __syncwarp();
         };
         while (ok && it.next()) {
@@ -443,109 +454,117 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 return lane < ppt && index < used ? page_at(a, it.b, index) : -2;
             };
             int pg = page_of(it.tile0);
-            for (int t = it.tile0; ok && t < it.tile0 + it.n; ++t) {
+            for (int t = it.tile0; t < it.tile0 + it.n; ++t) {
                 const int ahead = t + 1 < it.tile0 + it.n ? page_of(t + 1) : -2;
                 const bool good = pg >= 0 && pg < a.num_pages;
-                if (!good && pg != -2) atomicOr(status, kStatusInvalid);
+                if (kv == 0 && !good && pg != -2) atomicOr(status, kStatusInvalid);
                 uint32_t ks = 0, vs = 0;
-                if (good) {
+                if (kv == 0 && good) {
                     const int64_t cell = static_cast<int64_t>(pg) * a.Hkv + head;
                     ks = a.k_scales[cell];
                     vs = a.v_scales[cell];
                 }
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, good)) * (a.page * D);
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int s = slot % S;
-                    if (slot >= S && !wait(bar_kv_empty + s, ((slot / S) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar_kv_full + s, bytes);
-                        if (kv) mbar_arrive(bar_kv_full + s);
-                    }
-                    __syncwarp();
-                    if (good)
-                        tma_load_3d(sRing + s * C::kTileBytes + lane * a.page * D, kv ? &tmV : &tmK, bar_kv_full + s, 0, 0,
-                                    pg * a.Hkv + head);
-                    __syncwarp();
-                    if (kv == 0 && slot > 0) publish(slot - 2);
-                    ++slot;
+                if (2 * n + kv >= S && !wait(bar_kv_empty + at, phase ^ 1)) {
+                    ok = false;
+                    break;
                 }
-                late_ks = ks;
-                late_vs = vs;
-                late_good = good;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar_kv_full + at, bytes);
+                    if (kv == 1) mbar_arrive(bar_kv_full + at);
+                }
+                __syncwarp();
+                if (good)
+                    tma_load_3d(sRing + at * C::kTileBytes + lane * a.page * D, tm, bar_kv_full + at, 0, 0,
+                                pg * a.Hkv + head);
+                __syncwarp();
+                if (kv == 0) {
+                    if (n > 0) publish(n - 1);
+                    late_ks = ks;
+                    late_vs = vs;
+                    late_good = good;
+                    late_at = at;
+                }
                 pg = ahead;
+                ++n;
+                at += 2;
+                if (at >= S) {
+                    at -= S;
+                    phase ^= 1;
+                }
             }
         }
-        if (slot > 0) publish((slot - 1) & ~1);
+        if (kv == 0 && n > 0) publish(n - 1);
         // Every copy issued must land before the block exits.
         int dummy = 0;
-        for (int i = max(0, slot - S); i < slot; ++i)
+        for (int i = max(kv, 2 * n + kv - S); i < 2 * n + kv; i += 2)
             mbar_wait_bounded(bar_kv_full + i % S, (i / S) & 1, &dummy, status, kStatusTimeout, kTimeoutNs);
         __syncwarp();
     } else if (warp == 5) {
-        // ---------------------------------------------------------------- MMA issuer
-        const bool leader = elect_one_sync();
-        constexpr uint32_t kIdescS = f8_idesc(128, NC, false, false);
-        constexpr uint32_t kIdescO = f8_idesc(D, C::NO, true, true);
-        const uint64_t qd = smem_desc(smem_u32(sQ), 16, C::kSbo, C::kLayout);
-        const uint64_t rd = smem_desc(smem_u32(sRing), 16, C::kSbo, C::kLayout);
-        // P: 16-column chunks kTile * 16 bytes apart, in them 8 tokens of 16 bytes, then the next 8
-        const uint64_t pd = smem_desc(smem_u32(sP), 128, kTile * 16, kLayoutNone);
-        auto kv_ready = [&](int i) { return wait(bar_kv_full + i % S, (i / S) & 1); };
-        // S(n) of the piece that it belongs to
-        auto issue_s = [&](int n) -> bool {
-            const int i = 2 * n, s = i % S;
-            if (!kv_ready(i)) return false;
-            if (n >= 2 && !wait(bar_s_empty + (n & 1), (n / 2 - 1) & 1)) return false;
-            tc_fence_after_sync();
-            if (leader) {
-                const uint64_t kd = rd + static_cast<uint32_t>(s * (C::kTileBytes >> 4));
+        // ---------------------------------------------------------------- MMA issuer: one thread, whose waits cost less
+        if (elect_one_sync()) {
+            constexpr uint32_t kIdescS = f8_idesc(128, C::NS, false, false);
+            constexpr uint32_t kIdescO = f8_idesc(D, C::NO, true, true);
+            const uint64_t qd = smem_desc(smem_u32(sQ), 16, C::kSbo, C::kLayout);
+            const uint64_t rd = smem_desc(smem_u32(sRing), 16, C::kSbo, C::kLayout);
+            // P: 16-column chunks kTile * 16 bytes apart, in them 8 tokens of 16 bytes, then the next 8
+            const uint64_t pd = smem_desc(smem_u32(sP), 128, kTile * 16, kLayoutNone);
+            auto wait1 = [&](uint64_t* bar, uint32_t parity) -> bool {
+                return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status);
+            };
+            // Ring places and phases of the next K and the next V tile: every other place, S apart from the same.
+            int k_at = 0, v_at = 1;
+            uint32_t k_phase = 0, v_phase = 0;
+            auto advance = [](int& at, uint32_t& phase) {
+                at += 2;
+                if (at >= S) {
+                    at -= S;
+                    phase ^= 1;
+                }
+            };
+            // S(n) of the piece that it belongs to.  Its columns are free: PV(n - 2) has been issued, so P(n - 2) was
+            // there, and every thread had read S(n - 2) before it handed over its part of P.
+            auto issue_s = [&](int n) -> bool {
+                if (!wait1(bar_kv_full + k_at, k_phase)) return false;
+                tc_fence_after_sync();
+                const uint64_t kd = rd + static_cast<uint32_t>(k_at * (C::kTileBytes >> 4));
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-                    for (int kk = 0; kk < D / 32; ++kk)
-                        tc_mma_f8(tbase + (n & 1) * NC, kd + 2 * kk, qd + part * (C::kQBytes >> 4) + 2 * kk, kIdescS,
-                                  part > 0 || kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < D / 32; ++kk)
+                    tc_mma_f8(tbase + (n & 1) * C::NS, kd + 2 * kk, qd + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
                 tc_commit(bar_s_full + (n & 1));
-                tc_commit(bar_kv_empty + s);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto issue_pv = [&](int n, bool first) -> bool {
-            const int i = 2 * n + 1, s = i % S;
-            if (!kv_ready(i) || !wait(bar_p_full, n & 1)) return false;
-            tc_fence_after_sync();
-            if (leader) {
-                const uint64_t vd = rd + static_cast<uint32_t>(s * (C::kTileBytes >> 4));
+                tc_commit(bar_kv_empty + k_at);
+                advance(k_at, k_phase);
+                return true;
+            };
+            auto issue_pv = [&](int n, bool first) -> bool {
+                if (!wait1(bar_kv_full + v_at, v_phase) || !wait1(bar_p_full + (n & 1), (n >> 1) & 1)) return false;
+                tc_fence_after_sync();
+                const uint64_t vd = rd + static_cast<uint32_t>(v_at * (C::kTileBytes >> 4));
+                const uint64_t pn = pd + (C::kPBuffers == 2 ? (n & 1) * (C::kPBytes >> 4) : 0);
 #pragma unroll
                 for (int kk = 0; kk < kTile / 32; ++kk)
-                    tc_mma_f8(tbase + col_o, vd + kk * ((32 * D) >> 4), pd + kk * ((32 * 16) >> 4), kIdescO,
+                    tc_mma_f8(tbase + col_o, vd + kk * ((32 * D) >> 4), pn + kk * ((32 * 16) >> 4), kIdescO,
                               first && kk == 0 ? 0u : 1u);
-                tc_commit(bar_pv_done);
-                tc_commit(bar_kv_empty + s);
+                tc_commit(bar_pv_done + (n & 1));
+                tc_commit(bar_kv_empty + v_at);
+                advance(v_at, v_phase);
+                return true;
+            };
+            int n = 0;  // running number of the tile
+            bool ok = true;
+            for (int k = 0; ok && it.next(); ++k) {
+                ok = wait1(bar_q_full, k & 1) && issue_s(n);
+                for (int i = 0; ok && i < it.n; ++i) {
+                    if (i + 1 < it.n) ok = issue_s(n + 1);
+                    else tc_commit(bar_q_empty);
+                    ok = ok && issue_pv(n, i == 0);
+                    ++n;
+                }
             }
-            __syncwarp();
-            return true;
-        };
-        int n = 0;  // running number of the tile
-        bool ok = true;
-        for (int k = 0; ok && it.next(); ++k) {
-            ok = wait(bar_q_full, k & 1) && issue_s(n);
-            for (int i = 0; ok && i < it.n; ++i) {
-                if (i + 1 < it.n) ok = issue_s(n + 1);
-                else if (leader) tc_commit(bar_q_empty);
-                __syncwarp();
-                ok = ok && issue_pv(n, i == 0);
-                ++n;
-            }
+            tc_commit(bar_drain);
+            int dummy = 0;
+            mbar_wait_bounded(bar_drain, 0, &dummy, status, kStatusTimeout, kTimeoutNs);
         }
-        if (leader) tc_commit(bar_drain);
-        __syncwarp();
-        int dummy = 0;
-        mbar_wait_bounded(bar_drain, 0, &dummy, status, kStatusTimeout, kTimeoutNs);
         __syncwarp();
     } else if (warp == 6) {
         // ---------------------------------------------------------------- Q: a row (head) at a time, D / 32 channels a lane
@@ -599,12 +618,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 if (lane < R) sCol[(k & 1) * NC + g0 + lane] = my_col;
 #pragma unroll
                 for (int g = 0; g < R; ++g) {
-                    // swizzled like a TMA tile of D-byte rows
-                    const int byte = lane * E, row = g0 + g;
-                    const int chunk = D == 128 ? (byte >> 4) ^ (row & 7) : (byte >> 4) ^ ((row >> 1) & 3);
+                    const int byte = lane * E;
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
-                        uint8_t* at8 = sQ + part * C::kQBytes + row * D + chunk * 16 + (byte & 15);
+                        // swizzled like a TMA tile of D-byte rows
+                        const int row = part * GC + g0 + g;
+                        const int chunk = D == 128 ? (byte >> 4) ^ (row & 7) : (byte >> 4) ^ ((row >> 1) & 3);
+                        uint8_t* at8 = sQ + row * D + chunk * 16 + (byte & 15);
                         if constexpr (E == 4) *reinterpret_cast<uint32_t*>(at8) = parts[g][part];
                         else *reinterpret_cast<uint16_t*>(at8) = static_cast<uint16_t>(parts[g][part]);
                     }
@@ -621,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // (the flag makes the others give up at once) and the run goes on to its end, its results unspecified.
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
         const uint32_t t_o = tbase + lane_base + col_o;
+        auto wait_pv = [&](int m) { wait(bar_pv_done + (m & 1), (m >> 1) & 1); };
         int n = 0;
         int4 to_join = make_int4(-1, 0, 0, 0);  // sequence, first head, heads and slot, last block with a part
         for (int k = 0; it.next(); ++k) {
@@ -641,13 +662,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 tc_fence_after_sync();
                 float w[GC];  // log2 of the weights, relative to the bases
                 {
-                    uint32_t r[GC];
-                    tmem_ld<GC>(tbase + lane_base + (n & 1) * NC, r);
+                    // the smallest part first
+                    uint32_t r[C::NS];
+                    tmem_ld<C::NS>(tbase + lane_base + (n & 1) * C::NS, r);
 #pragma unroll
-                    for (int g = 0; g < GC; ++g) w[g] = __uint_as_float(r[g]);
+                    for (int g = 0; g < GC; ++g) {
+                        w[g] = __uint_as_float(r[(PARTS - 1) * GC + g]);
+#pragma unroll
+                        for (int part = PARTS - 2; part >= 0; --part) w[g] += __uint_as_float(r[part * GC + g]);
+                    }
                 }
-                tc_fence_before_sync();
-                mbar_arrive(bar_s_empty + (n & 1));
                 // S is there, so its K tile's barrier has completed: the exponents are too
                 const uint2 sc = sScale[n % C::kScaleRing * 8 + (tid >> P)];
                 const bool valid = t * kTile + tid < it.len && sc.y >= 0x100u;
@@ -703,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     fresh = ev_tile == 0 && fresh;
                     ev = ev_new;
                     if (!first) {
-                        wait(bar_pv_done, (n - 1) & 1);
+                        wait_pv(n - 1);
                         tc_fence_after_sync();
 #pragma unroll
                         for (int c = 0; c < C::NO / 16; ++c) {
@@ -711,8 +735,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             tmem_ld<16>(t_o + 16 * c, r);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                const int g = (16 * c + i) % NC;
-                                r[i] = g < GC ? __float_as_uint(__uint_as_float(r[i]) * alpha[g < GC ? g : 0]) : 0u;
+                                const int col = 16 * c + i;
+                                r[i] = col < kPParts * GC ? __float_as_uint(__uint_as_float(r[i]) * alpha[col % GC]) : 0u;
                             }
                             tmem_st16(t_o + 16 * c, r);
                         }
@@ -722,44 +746,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
                 // P in units of 2^ev: weights times 2^(own exponent - ev) * 32
                 const float vf = valid ? pow2_neg(ev - my_ev) * kPUnit : 0.f;
-                uint8_t* pb = sP + tid * 16;
+                uint8_t* pb = sP + (C::kPBuffers == 2 ? (n & 1) * C::kPBytes : 0) + tid * 16;
+                uint32_t pw[C::NO / 4];  // four columns a word
 #pragma unroll
-                for (int c = 0; c < NC / 16; ++c) {
-                    uint32_t pw[kPParts][4];
+                for (int i = kPParts * GC / 4; i < C::NO / 4; ++i) pw[i] = 0;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (16 * c + 4 * q >= GC) {
+                for (int q = 0; q < GC / 4; ++q) {
+                    float x[4];
 #pragma unroll
-                            for (int part = 0; part < kPParts; ++part) pw[part][q] = 0;
-                            continue;
-                        }
-                        float x[4];
+                    for (int i = 0; i < 4; ++i) {
+                        const float pr = ex2_approx(w[4 * q + i]);
+                        l[4 * q + i] += pr;
+                        x[i] = pr * vf;
+                    }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int g = (16 * c + 4 * q + i) % GC;
-                            const float pr = ex2_approx(w[g]);
-                            l[g] += pr;
-                            x[i] = pr * vf;
-                        }
+                    for (int part = 0; part < kPParts; ++part) {
+                        const uint32_t lo = pack_e4m3x2(x[0], x[1]), hi = pack_e4m3x2(x[2], x[3]);
+                        pw[part * (GC / 4) + q] = lo | hi << 16;
+                        if (part + 1 < kPParts) {
+                            float v[4];
+                            unpack_e4m3x2(lo, v[0], v[1]);
+                            unpack_e4m3x2(hi, v[2], v[3]);
 #pragma unroll
-                        for (int part = 0; part < kPParts; ++part) {
-                            const uint32_t lo = pack_e4m3x2(x[0], x[1]), hi = pack_e4m3x2(x[2], x[3]);
-                            pw[part][q] = lo | hi << 16;
-                            if (part + 1 < kPParts) {
-                                float v[4];
-                                unpack_e4m3x2(lo, v[0], v[1]);
-                                unpack_e4m3x2(hi, v[2], v[3]);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) x[i] = (x[i] - v[i]) * 16.f;
-                            }
+                            for (int i = 0; i < 4; ++i) x[i] = (x[i] - v[i]) * 16.f;
                         }
                     }
-                    if (n > 0) wait(bar_pv_done, (n - 1) & 1);  // PV(n - 1) has read the buffer
-#pragma unroll
-                    for (int part = 0; part < kPParts; ++part)
-                        *reinterpret_cast<uint4*>(pb + (part * (NC / 16) + c) * (kTile * 16)) =
-                            make_uint4(pw[part][0], pw[part][1], pw[part][2], pw[part][3]);
                 }
+                // The buffer is free: with two of them PV(n - 2) has read it, whose products came before those of S(n).
+                if (C::kPBuffers == 1 && n > 0) wait_pv(n - 1);
+#pragma unroll
+                for (int c = 0; c < C::NO / 16; ++c)
+                    *reinterpret_cast<uint4*>(pb + c * (kTile * 16)) =
+                        make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
                 // V rows of no token: zero, so that 0 * (what they hold) is 0.
                 if (__any_sync(0xffffffffu, !valid)) {
                     const int i = 2 * n + 1, sl = i % S;
@@ -772,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
-                mbar_arrive(bar_p_full);
+                mbar_arrive(bar_p_full + (n & 1));
             }
             // End of the piece: the row sums over the tile's threads, then O^T / l.
             float* sum = sMax;  // free: the last maxima have been read
@@ -783,17 +801,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 if (lane == g) keep = v;
             }
             if (lane < GC) sum[lane * 4 + warp] = keep;
-            wait(bar_pv_done, (n - 1) & 1);
+            wait_pv(n - 1);
             tc_fence_after_sync();
             named_barrier_sync(2, 128);
             float o[GC];
+            {
+                uint32_t r[C::NO];
+                tmem_ld<C::NO>(t_o, r);
 #pragma unroll
-            for (int part = kPParts - 1; part >= 0; --part) {
-                uint32_t r[GC];
-                tmem_ld<GC>(t_o + part * NC, r);
+                for (int part = kPParts - 1; part >= 0; --part)
 #pragma unroll
-                for (int g = 0; g < GC; ++g)
-                    o[g] = part == kPParts - 1 ? __uint_as_float(r[g]) : fmaf(o[g], 1.f / 16.f, __uint_as_float(r[g]));
+                    for (int g = 0; g < GC; ++g) {
+                        const float x = __uint_as_float(r[part * GC + g]);
+                        o[g] = part == kPParts - 1 ? x : fmaf(o[g], 1.f / 16.f, x);
+                    }
             }
             tc_fence_before_sync();
             // Lane g: head g's sum of weights, what O is multiplied by, and log2 of the sum.
