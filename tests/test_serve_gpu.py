@@ -507,6 +507,16 @@ def test_attend_many_sequences():
     check_attend(randn(g, 900, 4, 64), cache, table, lens)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("heads", [1, 3, 4, 5, 8, 9, 15, 16, 17])
+def test_attend_every_number_of_heads(heads, dtype, d):
+    """The parts of queries and weights share the columns of a product with the heads, up to 16 of them a block."""
+    g, lens = gen(heads + d), [129, 1, 0, 700, 64, 2100]
+    cache, table = fill(g, lens, 2, 32, d, dtype)
+    check_attend(randn(g, len(lens), 2 * heads, d, dtype=dtype, scale=2.0), cache, table, lens)
+
+
 @pytest.mark.parametrize("Hkv,d,page,dtype", [(24, 64, 16, FP), (8, 128, 64, BF)])
 def test_attend_blocks_of_many_one_tile_pieces(Hkv, d, page, dtype):
     """Queries, products and weights change hands at every tile, over and over: no wait may miss its phase."""
